@@ -258,9 +258,9 @@ def _plain_select_grad(c, s):
 
 
 def _sequence_sums(x, off):
-    """Each sequence's sums of the rows of x: differences of running sums, in 64 bits."""
-    ahead = torch.nn.functional.pad(x.cumsum(dim=0, dtype=torch.float64), (0, 0, 1, 0))
-    return ahead[off[1:].long()] - ahead[off[:-1].long()]
+    """Each sequence's sums of the rows of x, as a product with the sequences' membership."""
+    inside = _of_sequence(off, x.shape[0]) == torch.arange(off.numel() - 1, device=DEV)[:, None]
+    return (inside.float() @ x).double()
 
 
 def _plain_balance(c, s):
