@@ -99,7 +99,10 @@ typedef struct {
 } moe_ffn_weights_t;
 
 /* Workspace stages for moe_workspace_bytes. */
-enum { MOE_WS_DISPATCH = 0, MOE_WS_FFN = 1, MOE_WS_COMBINE = 2, MOE_WS_ROUTE = 3, MOE_WS_BACKWARD = 4 };
+enum {
+    MOE_WS_DISPATCH = 0, MOE_WS_FFN = 1, MOE_WS_COMBINE = 2, MOE_WS_ROUTE = 3, MOE_WS_BACKWARD = 4,
+    MOE_WS_ROUTER_LOGITS = 5, MOE_WS_ROUTER_GRAD = 6, MOE_WS_BACKWARD_SAVED = 7
+};
 
 /*
  * Router, biased top-k choice and combine weights (DeepSeek V3 From Scratch,
@@ -314,6 +317,184 @@ moe_status_t moe_backward(const moe_desc_t *desc, const void *x, const float *w_
                           float *dw_router, float *dw_gate, float *dw_up, float *dw_down, float *ds_gate,
                           float *ds_up, float *ds_down, float *dg, void *workspace, size_t ws_bytes,
                           void *stream);
+
+/* ------------------------------------------------------------------------
+ * Routing from logits: the router's product on its own, the choice of experts
+ * by other rules than moe_route's, the loss that balances each sequence, and
+ * their gradients.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The router's logits alone: logits[t, e] = x_t . w_router[e], fp32, by the
+ * arithmetic of moe_route.
+ *   x        [T, d]  act type
+ *   w_router [E, d]  fp32
+ *   logits   [T, E]  fp32 out
+ *   workspace >= moe_workspace_bytes(desc, MOE_WS_ROUTER_LOGITS) bytes of
+ *            device memory (0 for fp32 activations; NULL allowed then)
+ */
+moe_status_t moe_router_logits(const moe_desc_t *desc, const void *x, const float *w_router, float *logits,
+                               void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Its gradient: dx = dx_in + dlogits . w_router, dw_router = dlogits^T . x.
+ *   dlogits   [T, E] fp32 (moe_select_backward)
+ *   dx_in     [T, d] fp32 or NULL (zero): the other gradients of x, for instance
+ *             moe_backward_saved's dx; may be dx itself
+ *   dx        [T, d] fp32 out
+ *   dw_router [E, d] fp32 out (written, not accumulated)
+ *   workspace >= moe_workspace_bytes(desc, MOE_WS_ROUTER_GRAD) bytes
+ * Deterministic.
+ */
+moe_status_t moe_router_logits_backward(const moe_desc_t *desc, const void *x, const float *w_router,
+                                        const float *dlogits, const float *dx_in, float *dx, float *dw_router,
+                                        void *workspace, size_t ws_bytes, void *stream);
+
+typedef enum { MOE_SIGMOID = 0, MOE_SOFTMAX = 1 } moe_score_t;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP_TWO = 1 } moe_group_score_t;
+
+/* The rule by which k of E experts are chosen for each of T tokens.
+ *   score        moe_score_t: s = sigmoid(logit), or softmax over the E logits
+ *   n_group      the experts are n_group runs of E / n_group (1: no groups)
+ *   topk_group   only the experts of the topk_group best groups can be chosen;
+ *                topk_group * (E / n_group) >= k
+ *   group_score  moe_group_score_t: a group's score is the largest of its
+ *                experts' biased scores, or the sum of the two largest
+ *   renorm       1: the weights are divided by their sum over the chosen
+ *   scale        factor on the weights
+ *   logits       moe_dtype_t of the logits: MOE_F32 or MOE_BF16
+ * Any E up to 1024, k up to 64. */
+typedef struct {
+    int32_t T, E, k;
+    int32_t score;
+    int32_t n_group, topk_group, group_score;
+    int32_t renorm;
+    float scale;
+    int32_t logits;
+} moe_select_t;
+
+/*
+ * The choice and its combine weights, in one launch.
+ *   logits  [T, E], row t at logits + t * ld (ld >= E, in elements)
+ *   bias    [E] fp32 or NULL: added to the scores for the choice only
+ *   idx     [T, k] int32 out: ids ascending; the k largest s + bias among the
+ *           open groups; equal scores, of experts or groups, go to the lower id
+ *   weights [T, k] fp32 out: scale * s of each chosen expert, over the sum of
+ *           the chosen s with renorm (0 where that sum is 0)
+ * The choice is made by the scores in 64 bits (without a bias by the logits
+ * themselves, whose order is theirs), the weights are computed in fp32.  A
+ * logit of -inf has the score 0; a NaN score ranks behind every number, and
+ * a group with fewer than two numbers behind every group with two
+ * (MOE_GROUP_TOP_TWO, groups of more than one).  idx always holds k distinct
+ * ids in [0, E).
+ * With E = 256, k = 8 idx and weights go straight into moe_dispatch and
+ * moe_combine.
+ */
+moe_status_t moe_select(const moe_select_t *sel, const void *logits, int64_t ld, const float *bias, int32_t *idx,
+                        float *weights, void *stream);
+
+/*
+ * Gradient with respect to the logits, dlogits [T, E] fp32 (written): through
+ * the weights, where dweights [T, k] is given, and through the balance loss,
+ * where seq_offsets is; at least one of the two.  The choice carries no
+ * gradient.
+ *   idx          [T, k] from moe_select (distinct in a row; an id outside [0, E)
+ *                is skipped); needed with dweights
+ *   seq_offsets  [n_seq + 1], load [n_seq, E]: from moe_balance_loss
+ *   dloss        [n_seq] fp32: gradient of each sequence's loss
+ *   alpha        as for moe_balance_loss
+ * Rows outside every sequence get no balance gradient.
+ */
+moe_status_t moe_select_backward(const moe_select_t *sel, const void *logits, int64_t ld, const int32_t *idx,
+                                 const float *dweights, const int32_t *seq_offsets, int32_t n_seq, const float *load,
+                                 const float *dloss, float alpha, float *dlogits, void *stream);
+
+/*
+ * Sequence-wise balance loss.  Tokens seq_offsets[q] .. seq_offsets[q+1]-1 are
+ * sequence q, of n tokens; p_{t,e} = s_{t,e} / sum_i s_{t,i};
+ *   load_{q,e} = E / (k n) * (choices of e in q),  P_{q,e} = mean of p_{t,e},
+ *   loss_q = alpha * sum_e load_{q,e} P_{q,e}.
+ * A balanced sequence has the loss alpha.  load carries no gradient.
+ *   idx         [T, k] the choices that are counted (moe_select's, or others)
+ *   seq_offsets [n_seq + 1] int32 on the device, ascending, in [0, T]; empty
+ *               sequences are allowed (loss 0, load 0)
+ *   loss [n_seq], load [n_seq, E] fp32 out
+ *   workspace >= moe_balance_workspace_bytes(sel, n_seq) bytes
+ * Of the rule T, E, k, score and logits are read.  Deterministic.
+ */
+moe_status_t moe_balance_loss(const moe_select_t *sel, const void *logits, int64_t ld, const int32_t *idx,
+                              const int32_t *seq_offsets, int32_t n_seq, float alpha, float *loss, float *load,
+                              void *workspace, size_t ws_bytes, void *stream);
+size_t moe_balance_workspace_bytes(const moe_select_t *sel, int32_t n_seq);
+
+/* ------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits: what the backward needs of the forward
+ * (x, and y_perm with its T*k rows) kept in half the memory of bf16.
+ * ------------------------------------------------------------------------ */
+
+/* Formats of a saved activation [rows, cols].  The 8-bit ones hold one code per
+ * value and one E8M0 scale byte per 1x128 tile of a row (the last tile of a row
+ * may be shorter), scales [rows, ceil(cols/128)]: byte b stands for 2^(b-127),
+ * the smallest power of two at or above the tile's largest magnitude / 448
+ * (e4m3) or / 127 (int8), at least 2^-126, and 1 for an all-zero tile; the code
+ * is the value over the scale, rounded to nearest even.  e4m3 keeps small values
+ * of a tile to 3 bits, int8 keeps all of them to the same step.  A tile with an
+ * infinity or a NaN gets the byte 255 and reads back as NaN; a finite value
+ * whose rounded one is past fp32's largest reads back as infinity. */
+typedef enum { MOE_SAVED_BF16 = 0, MOE_SAVED_E4M3 = 1, MOE_SAVED_I8 = 2 } moe_saved_format_t;
+typedef struct {
+    const void *data;       /* bf16 values, or 8-bit codes [rows, cols] */
+    const uint8_t *scales;  /* the 8-bit formats only, else NULL */
+    int32_t format;         /* moe_saved_format_t */
+} moe_saved_t;
+
+/*
+ * Values to codes and back, rows and columns of any number.
+ *   type     MOE_F32 or MOE_BF16: of src and dst
+ *   src, dst [rows, cols], row r at + r * ld (ld >= cols, in elements); what
+ *            lies between the rows is neither read nor written
+ *   format   MOE_SAVED_E4M3 or MOE_SAVED_I8
+ *   codes    [rows, cols] bytes, scales [rows, ceil(cols/128)] bytes
+ */
+moe_status_t moe_checkpoint_pack(int64_t rows, int32_t cols, int32_t type, const void *src, int64_t ld, int32_t format,
+                                 uint8_t *codes, uint8_t *scales, void *stream);
+moe_status_t moe_checkpoint_unpack(int64_t rows, int32_t cols, int32_t type, const uint8_t *codes,
+                                   const uint8_t *scales, int32_t format, void *dst, int64_t ld, void *stream);
+
+/*
+ * Gradient of the weighted combine with respect to the routed outputs and the
+ * weights, from saved routed outputs:
+ *   dg[t, j] = dy[t] . y_perm[row_of[t*k + j]],  dy_perm[row_of[t*k + j]] = weights[t, j] dy[t]
+ *   dy      [T, d] fp32
+ *   y_perm  saved [T*k, d]
+ *   row_of, weights: as for moe_combine; an entry of row_of outside [0, T*k)
+ *           (a choice that was not dispatched) has no row: its dg is 0
+ *   dy_perm [T*k, d] bf16 out; rows that no entry names are left as they were
+ *   dg      [T, k] fp32 out
+ * dy, y_perm's data and dy_perm are 16-byte aligned.  Deterministic.
+ */
+moe_status_t moe_combine_backward(const moe_desc_t *desc, const float *dy, const moe_saved_t *y_perm,
+                                  const int32_t *row_of, const float *weights, void *dy_perm, float *dg, void *stream);
+
+/*
+ * moe_backward from saved activations, and with any router.
+ *   x       saved [T, d]; y_perm saved [T*k, d]
+ *   w_router, dw_router: NULL together where the choice did not come from
+ *           moe_route: dx then holds the experts' share alone, idx is not read
+ *           (NULL allowed), and dg (required) goes to moe_select_backward as
+ *           dweights and on to moe_router_logits_backward
+ * All else as for moe_backward; with both activations in bf16 and a w_router
+ * it is moe_backward, bit for bit.
+ *   workspace >= moe_workspace_bytes(desc, MOE_WS_BACKWARD_SAVED) bytes:
+ *   moe_backward's and one bf16 [T, d].
+ */
+moe_status_t moe_backward_saved(const moe_desc_t *desc, const moe_saved_t *x, const float *w_router,
+                                const int32_t *idx, const float *weights, const int32_t *offsets,
+                                const int32_t *row_src, const int32_t *row_of, const moe_ffn_weights_t *experts,
+                                const moe_ffn_weights_t *shared, const moe_saved_t *y_perm, const float *dy, float *dx,
+                                float *dw_router, float *dw_gate, float *dw_up, float *dw_down, float *ds_gate,
+                                float *ds_up, float *ds_down, float *dg, void *workspace, size_t ws_bytes,
+                                void *stream);
 
 /* Static, human-readable name of a status code. */
 const char *moe_status_str(moe_status_t status);

@@ -16,11 +16,20 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 MOE_OK, MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE, MOE_EHIP, MOE_ESCRATCH = range(6)
 MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
 MOE_WS_DISPATCH, MOE_WS_FFN, MOE_WS_COMBINE, MOE_WS_ROUTE, MOE_WS_BACKWARD = 0, 1, 2, 3, 4
+MOE_WS_ROUTER_LOGITS, MOE_WS_ROUTER_GRAD, MOE_WS_BACKWARD_SAVED = 5, 6, 7
+MOE_SIGMOID, MOE_SOFTMAX = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP_TWO = 0, 1
+MOE_SAVED_BF16, MOE_SAVED_E4M3, MOE_SAVED_I8 = 0, 1, 2
 DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "e4m3": MOE_E4M3}
+SCORES = {"sigmoid": MOE_SIGMOID, "softmax": MOE_SOFTMAX}
+GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP_TWO}
+SAVED_FORMATS = {"bf16": MOE_SAVED_BF16, "e4m3": MOE_SAVED_E4M3, "i8": MOE_SAVED_I8}
 
 EXPORTS = ("moe_route", "moe_dispatch", "moe_dispatch_noalloc", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_gate_up_rows",
            "moe_expert_down", "moe_combine", "moe_bias_update", "moe_backward", "moe_workspace_bytes",
-           "moe_status_str")
+           "moe_status_str", "moe_router_logits", "moe_router_logits_backward", "moe_select", "moe_select_backward",
+           "moe_balance_loss", "moe_balance_workspace_bytes", "moe_checkpoint_pack", "moe_checkpoint_unpack",
+           "moe_combine_backward", "moe_backward_saved")
 
 
 class MoeError(RuntimeError):
@@ -37,6 +46,16 @@ class Desc(ctypes.Structure):
 class FfnWeights(ctypes.Structure):
     _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("down", ctypes.c_void_p),
                 ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p)]
+
+
+class Select(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("logits", ctypes.c_int32)]
+
+
+class Saved(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int32)]
 
 
 _lib = None
@@ -65,6 +84,23 @@ def load(path: str = LIB_PATH):
     L.moe_bias_update.argtypes = [pd, vp, f32, vp, vp]
     L.moe_backward.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, pw, pw, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                vp, sz, vp]
+    i64, psel, psav = ctypes.c_int64, ctypes.POINTER(Select), ctypes.POINTER(Saved)
+    L.moe_router_logits.argtypes = [pd, vp, vp, vp, vp, sz, vp]
+    L.moe_router_logits_backward.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_select.argtypes = [psel, vp, i64, vp, vp, vp, vp]
+    L.moe_select_backward.argtypes = [psel, vp, i64, vp, vp, vp, i32, vp, vp, f32, vp, vp]
+    L.moe_balance_loss.argtypes = [psel, vp, i64, vp, vp, i32, f32, vp, vp, vp, sz, vp]
+    L.moe_balance_workspace_bytes.argtypes = [psel, i32]
+    L.moe_balance_workspace_bytes.restype = sz
+    L.moe_checkpoint_pack.argtypes = [i64, i32, i32, vp, i64, i32, vp, vp, vp]
+    L.moe_checkpoint_unpack.argtypes = [i64, i32, i32, vp, vp, i32, vp, i64, vp]
+    L.moe_combine_backward.argtypes = [pd, vp, psav, vp, vp, vp, vp, vp]
+    L.moe_backward_saved.argtypes = [pd, psav, vp, vp, vp, vp, vp, vp, pw, pw, psav, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                     vp, vp, sz, vp]
+    for fn in ("moe_router_logits", "moe_router_logits_backward", "moe_select", "moe_select_backward",
+               "moe_balance_loss", "moe_checkpoint_pack", "moe_checkpoint_unpack", "moe_combine_backward",
+               "moe_backward_saved"):
+        getattr(L, fn).restype = ctypes.c_int
     for fn in ("moe_route", "moe_dispatch", "moe_dispatch_noalloc", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_gate_up_rows",
                "moe_expert_down", "moe_combine", "moe_bias_update", "moe_backward"):
         getattr(L, fn).restype = ctypes.c_int
@@ -170,3 +206,230 @@ def moe_backward(ds, x, w_router, idx, weights, offsets, row_src, row_of, expert
 def moe_bias_update(ds, counts, gamma, bias, stream=None):
     _check("moe_bias_update", load().moe_bias_update(ctypes.byref(ds), _ptr(counts), gamma, _ptr(bias),
                                                      _stream(stream)))
+
+
+# ------------------------------------------------- routing from logits, checkpoints
+#
+# These entry points check their tensors (type, shape, contiguity, device) and
+# run on the device that holds them, whichever is current.
+
+def selection(T, E, k, score="sigmoid", n_group=1, topk_group=1, group_score="top2", renorm=True, scale=1.0,
+              logits="f32") -> Select:
+    """The rule by which k of E experts are chosen for each of T tokens (moe_select_t)."""
+    return Select(T, E, k, SCORES[score], n_group, topk_group, GROUP_SCORES[group_score], int(renorm), scale,
+                  DTYPES[logits])
+
+
+def saved(data, scales=None, fmt="bf16") -> Saved:
+    """A saved activation (moe_saved_t): bf16 values, or 8-bit codes and their tiles' scales."""
+    return Saved(data.data_ptr(), scales.data_ptr() if scales is not None else None, SAVED_FORMATS[fmt])
+
+
+def balance_workspace_bytes(sel: Select, n_seq: int) -> int:
+    return load().moe_balance_workspace_bytes(ctypes.byref(sel), n_seq)
+
+
+def _library():
+    return load()
+
+
+_STORAGE = None
+
+
+def _storage():
+    """The torch types a storage type travels in (bf16 also as its 16-bit patterns)."""
+    global _STORAGE
+    if _STORAGE is None:
+        import torch
+        _STORAGE = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16), MOE_E4M3: (torch.uint8,),
+                    "i32": (torch.int32,), "byte": (torch.uint8, torch.int8)}
+    return _STORAGE
+
+
+class _Call:
+    """Checks of one call's tensors, which have to lie on one GPU, and its launch there."""
+
+    def __init__(self, fn):
+        self.fn, self.device, self.elsewhere = fn, None, None
+
+    def refuse(self, what):
+        raise MoeError(self.fn, MOE_EINVAL, "MOE_EINVAL: " + what)
+
+    def ptr(self, name, t, kind, shape, optional=False):
+        """The address of a contiguous tensor of that type and shape."""
+        if t is None:
+            if not optional:
+                self.refuse(f"{name} is missing")
+            return None
+        if t.dtype not in _storage()[kind]:
+            self.refuse(f"{name} has type {t.dtype}")
+        if tuple(t.shape) != shape:
+            self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
+        if not t.is_contiguous():
+            self.refuse(f"{name} is not contiguous")
+        return self.on(name, t)
+
+    def rows(self, name, t, kind, shape):
+        """The address and row stride of a tensor whose rows are contiguous."""
+        if t is None:
+            self.refuse(f"{name} is missing")
+        if t.dtype not in _storage()[kind]:
+            self.refuse(f"{name} has type {t.dtype}")
+        if tuple(t.shape) != shape:
+            self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
+        ld = t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+        if (shape[1] > 1 and t.stride(1) != 1) or ld < shape[1]:
+            self.refuse(f"{name} has strides {tuple(t.stride())}: its rows have to be contiguous and apart")
+        return self.on(name, t), ld
+
+    def on(self, name, t):
+        device = t.device
+        if device != self.device:
+            if self.device is None and device.type == "cuda":
+                self.device = device
+            elif self.elsewhere is None:  # reported behind the types and shapes
+                self.elsewhere = f"{name} is on {device}" + (f", not {self.device}" if self.device is not None else "")
+        return t.data_ptr()
+
+    def workspace(self, t):
+        """Address and size of a workspace (None: none)."""
+        if t is None:
+            return None, 0
+        if not t.is_contiguous():
+            self.refuse("the workspace is not contiguous")
+        return self.on("the workspace", t), t.numel() * t.element_size()
+
+    def run(self, call, *args, stream=None):
+        import torch
+        if self.elsewhere is not None:
+            self.refuse(self.elsewhere)
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
+            self.refuse(f"the stream is on {stream.device}, not {self.device}")
+        if torch.cuda.current_device() == self.device.index:
+            st = call(*args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = call(*args, stream.cuda_stream)
+        _check(self.fn, st)
+
+
+def moe_router_logits(ds, x, w_router, logits, workspace=None, stream=None):
+    """logits [T, E] = x . w_router^T in fp32."""
+    c = _Call("moe_router_logits")
+    args = (c.ptr("x", x, ds.act, (ds.T, ds.d)), c.ptr("w_router", w_router, MOE_F32, (ds.E, ds.d)),
+            c.ptr("logits", logits, MOE_F32, (ds.T, ds.E)))
+    c.run(load().moe_router_logits, ctypes.byref(ds), *args, *c.workspace(workspace), stream=stream)
+
+
+def moe_router_logits_backward(ds, x, w_router, dlogits, dx_in, dx, dw_router, workspace=None, stream=None):
+    """dx = dx_in + dlogits . w_router (dx_in may be None, or dx itself), dw_router = dlogits^T . x."""
+    c = _Call("moe_router_logits_backward")
+    args = (c.ptr("x", x, ds.act, (ds.T, ds.d)), c.ptr("w_router", w_router, MOE_F32, (ds.E, ds.d)),
+            c.ptr("dlogits", dlogits, MOE_F32, (ds.T, ds.E)), c.ptr("dx_in", dx_in, MOE_F32, (ds.T, ds.d), True),
+            c.ptr("dx", dx, MOE_F32, (ds.T, ds.d)), c.ptr("dw_router", dw_router, MOE_F32, (ds.E, ds.d)))
+    c.run(load().moe_router_logits_backward, ctypes.byref(ds), *args, *c.workspace(workspace), stream=stream)
+
+
+def moe_select(sel: Select, logits, bias, idx, weights, stream=None):
+    """The choice of experts and its combine weights; logits [T, E] with any row stride, bias [E] or None."""
+    c = _Call("moe_select")
+    p, ld = c.rows("logits", logits, sel.logits, (sel.T, sel.E))
+    args = (c.ptr("bias", bias, MOE_F32, (sel.E,), True), c.ptr("idx", idx, "i32", (sel.T, sel.k)),
+            c.ptr("weights", weights, MOE_F32, (sel.T, sel.k)))
+    c.run(load().moe_select, ctypes.byref(sel), p, ld, *args, stream=stream)
+
+
+def moe_select_backward(sel: Select, logits, idx, dweights, dlogits, seq_offsets=None, load=None, dloss=None, alpha=0.0,
+                        stream=None):
+    """dlogits [T, E] through the weights (dweights [T, k], or None) and the balance loss (seq_offsets, load and dloss
+    of moe_balance_loss, or None)."""
+    c = _Call("moe_select_backward")
+    p, ld = c.rows("logits", logits, sel.logits, (sel.T, sel.E))
+    n = seq_offsets.numel() - 1 if seq_offsets is not None else 0
+    on = seq_offsets is None
+    args = (c.ptr("idx", idx, "i32", (sel.T, sel.k), dweights is None),
+            c.ptr("dweights", dweights, MOE_F32, (sel.T, sel.k), True),
+            c.ptr("seq_offsets", seq_offsets, "i32", (n + 1,), True), n,
+            c.ptr("load", load, MOE_F32, (n, sel.E), on), c.ptr("dloss", dloss, MOE_F32, (n,), on), alpha,
+            c.ptr("dlogits", dlogits, MOE_F32, (sel.T, sel.E)))
+    c.run(_library().moe_select_backward, ctypes.byref(sel), p, ld, *args, stream=stream)
+
+
+def moe_balance_loss(sel: Select, logits, idx, seq_offsets, alpha, loss, load, workspace, stream=None):
+    """The sequence-wise balance loss [n_seq] and each expert's load [n_seq, E]."""
+    c = _Call("moe_balance_loss")
+    p, ld = c.rows("logits", logits, sel.logits, (sel.T, sel.E))
+    if seq_offsets is None or seq_offsets.numel() < 2:
+        c.refuse("seq_offsets holds no sequence")
+    n = seq_offsets.numel() - 1
+    args = (c.ptr("idx", idx, "i32", (sel.T, sel.k)), c.ptr("seq_offsets", seq_offsets, "i32", (n + 1,)), n, alpha,
+            c.ptr("loss", loss, MOE_F32, (n,)), c.ptr("load", load, MOE_F32, (n, sel.E)))
+    c.run(_library().moe_balance_loss, ctypes.byref(sel), p, ld, *args, *c.workspace(workspace), stream=stream)
+
+
+def _plain_type(c, name, t):
+    """MOE_F32 or MOE_BF16 of a plain 2-D tensor."""
+    if t is None or t.dim() != 2:
+        c.refuse(f"{name} has to be a matrix")
+    for kind in (MOE_F32, MOE_BF16):
+        if t.dtype in _storage()[kind]:
+            return kind
+    c.refuse(f"{name} has type {t.dtype}")
+
+
+def _codes(c, codes, scales, fmt, rows, cols):
+    if fmt not in ("e4m3", "i8"):
+        c.refuse(f"format {fmt!r}")
+    return (c.ptr("codes", codes, "byte", (rows, cols)),
+            c.ptr("scales", scales, MOE_E4M3, (rows, (cols + 127) // 128)))
+
+
+def moe_checkpoint_pack(src, codes, scales, fmt, stream=None):
+    """src [rows, cols] (fp32 or bf16, any row stride) as 8-bit codes [rows, cols] and scales [rows, ceil(cols/128)];
+    fmt: "e4m3" or "i8"."""
+    c = _Call("moe_checkpoint_pack")
+    kind = _plain_type(c, "src", src)
+    rows, cols = src.shape
+    p, ld = c.rows("src", src, kind, (rows, cols))
+    q, s = _codes(c, codes, scales, fmt, rows, cols)
+    c.run(load().moe_checkpoint_pack, rows, cols, kind, p, ld, SAVED_FORMATS[fmt], q, s, stream=stream)
+
+
+def moe_checkpoint_unpack(codes, scales, fmt, dst, stream=None):
+    """The values of 8-bit codes into dst [rows, cols] (fp32 or bf16, any row stride)."""
+    c = _Call("moe_checkpoint_unpack")
+    kind = _plain_type(c, "dst", dst)
+    rows, cols = dst.shape
+    q, s = _codes(c, codes, scales, fmt, rows, cols)
+    p, ld = c.rows("dst", dst, kind, (rows, cols))
+    c.run(load().moe_checkpoint_unpack, rows, cols, kind, q, s, SAVED_FORMATS[fmt], p, ld, stream=stream)
+
+
+def moe_combine_backward(ds, dy, y_perm: Saved, row_of, weights, dy_perm, dg, stream=None):
+    """The combine's gradient from saved routed outputs: dy_perm [T*k, d] bf16 and dg [T, k]."""
+    c = _Call("moe_combine_backward")
+    args = (c.ptr("dy", dy, MOE_F32, (ds.T, ds.d)), ctypes.byref(y_perm), c.ptr("row_of", row_of, "i32", (ds.T * ds.k,)),
+            c.ptr("weights", weights, MOE_F32, (ds.T, ds.k)), c.ptr("dy_perm", dy_perm, MOE_BF16, (ds.T * ds.k, ds.d)),
+            c.ptr("dg", dg, MOE_F32, (ds.T, ds.k)))
+    c.run(load().moe_combine_backward, ctypes.byref(ds), *args, stream=stream)
+
+
+def moe_backward_saved(ds, x: Saved, w_router, idx, weights, offsets, row_src, row_of, experts: FfnWeights,
+                       shared: FfnWeights, y_perm: Saved, dy, grads: dict, workspace, stream=None):
+    """moe_backward from saved activations; w_router None leaves the router's share to the caller (grads then has no
+    dw_router and has dg)."""
+    c = _Call("moe_backward_saved")
+    A, T, d, E, I = ds.T * ds.k, ds.T, ds.d, ds.E, ds.I
+    own = w_router is None
+    head = (ctypes.byref(x), c.ptr("w_router", w_router, MOE_F32, (E, d), True),
+            c.ptr("idx", idx, "i32", (T, ds.k), own), c.ptr("weights", weights, MOE_F32, (T, ds.k)),
+            c.ptr("offsets", offsets, "i32", (E + 1,)), c.ptr("row_src", row_src, "i32", (A,)),
+            c.ptr("row_of", row_of, "i32", (A,)), ctypes.byref(experts), ctypes.byref(shared), ctypes.byref(y_perm),
+            c.ptr("dy", dy, MOE_F32, (T, d)))
+    out = [c.ptr(n, grads.get(n), MOE_F32, s, n == "dg" or (n == "dw_router" and own))
+           for n, s in (("dx", (T, d)), ("dw_router", (E, d)), ("dw_gate", (E, I, d)), ("dw_up", (E, I, d)),
+                        ("dw_down", (E, d, I)), ("ds_gate", (I, d)), ("ds_up", (I, d)), ("ds_down", (d, I)),
+                        ("dg", (T, ds.k)))]
+    c.run(load().moe_backward_saved, ctypes.byref(ds), *head, *out, *c.workspace(workspace), stream=stream)

@@ -505,7 +505,9 @@ __global__ __launch_bounds__(256) void k_bwd_dwr_sum(int64_t n, const float *__r
     dwr[i] = acc;
 }
 
-// dx[t] += dxs[t] + sum_j dxp[row_of[t*8 + j]] (j ascending), 4 columns per thread.
+// dx[t] += dxs[t] + sum_j dxp[row_of[t*8 + j]] (j ascending), 4 columns per
+// thread; !ADD: dx is written.
+template <bool ADD>
 __global__ __launch_bounds__(256) void k_bwd_dx(int T, int d, const float *__restrict__ dxs,
                                                 const float *__restrict__ dxp, const int32_t *__restrict__ row_of,
                                                 float *__restrict__ dx) {
@@ -514,9 +516,8 @@ __global__ __launch_bounds__(256) void k_bwd_dx(int T, int d, const float *__res
     if (i >= (int64_t)T * w4) return;
     const int64_t t = i / w4;
     const int c = (int)(i - t * w4) * 4;
-    f32x4 v = *reinterpret_cast<const f32x4 *>(dx + t * d + c);
-    const f32x4 s = *reinterpret_cast<const f32x4 *>(dxs + t * d + c);
-    v += s;
+    f32x4 v = *reinterpret_cast<const f32x4 *>(dxs + t * d + c);
+    if (ADD) v = *reinterpret_cast<const f32x4 *>(dx + t * d + c) + v;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int r = row_of[t * 8 + j];
@@ -589,9 +590,12 @@ hipError_t zero_empty(int64_t per, const int32_t *off, float *out, hipStream_t s
     return hipGetLastError();
 }
 
-hipError_t dx(int T, int d, const float *dxs, const float *dxp, const int32_t *row_of, float *dx_out, hipStream_t s) {
+hipError_t dx(int T, int d, const float *dxs, const float *dxp, const int32_t *row_of, float *dx_out, bool add,
+              hipStream_t s) {
     const int64_t n = (int64_t)T * (d / 4);
-    hipLaunchKernelGGL(k_bwd_dx, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, T, d, dxs, dxp, row_of, dx_out);
+    const dim3 grid((unsigned)((n + 255) / 256));
+    if (add) hipLaunchKernelGGL(k_bwd_dx<true>, grid, dim3(256), 0, s, T, d, dxs, dxp, row_of, dx_out);
+    else hipLaunchKernelGGL(k_bwd_dx<false>, grid, dim3(256), 0, s, T, d, dxs, dxp, row_of, dx_out);
     return hipGetLastError();
 }
 
@@ -790,8 +794,9 @@ hipError_t launch_backward(const BackwardArgs &a, void *ws, hipStream_t s) {
     }
 
     // 1. combine backward
-    CHK(bwd::combine(T, d, a.dy, static_cast<const uint16_t *>(a.y_perm), a.row_of, a.weights, w.dyo, dys, dg, false,
-                     s));
+    CHK(a.y_saved.data ? launch_combine_backward(T, d, a.dy, a.y_saved, a.row_of, a.weights, w.dyo, dys, dg, false, s)
+                       : bwd::combine(T, d, a.dy, static_cast<const uint16_t *>(a.y_perm), a.row_of, a.weights, w.dyo,
+                                      dys, dg, false, s));
     // The data-gradient GEMMs (and the recompute) are NT GEMMs grouped over
     // M: the forward's persistent 256x256-tile kernel with an fp32 epilogue
     // when the groups are large enough, else k_bgemm.
@@ -870,10 +875,12 @@ hipError_t launch_backward(const BackwardArgs &a, void *ws, hipStream_t s) {
                Tp));
     }
     // 7. router: dl and its share of dx (written), then the router gradient
-    CHK(bwd::router(T, d, x, a.w_router, a.idx, dg, w.dl, a.dx, s));
-    CHK(bwd::dwr(d, a.offsets, a.row_src, w.dl, x, w.dwr_part, a.dw_router, s));
+    if (a.w_router) {
+        CHK(bwd::router(T, d, x, a.w_router, a.idx, dg, w.dl, a.dx, s));
+        CHK(bwd::dwr(d, a.offsets, a.row_src, w.dl, x, w.dwr_part, a.dw_router, s));
+    }
     // 8. dx += shared + routed input gradients
-    CHK(bwd::dx(T, d, dxs, w.dxi, a.row_of, a.dx, s));
+    CHK(bwd::dx(T, d, dxs, w.dxi, a.row_of, a.dx, a.w_router != nullptr, s));
 #undef CHK
     return hipSuccess;
 }

@@ -590,8 +590,9 @@ hipError_t launch_backward_fp8(const BackwardArgs &a, void *ws, hipStream_t s) {
     CHK(tscale(I, d, 1, sh.s_up, w.sguTs, 2 * I / 128, I / 128, s));
 
     // 1. combine backward (fp32 output gradients) and x per 1x128 tile of d
-    CHK(bwd::combine(T, d, a.dy, static_cast<const uint16_t *>(a.y_perm), a.row_of, a.weights, w.dyo, dys, dg, true,
-                     s));
+    CHK(a.y_saved.data ? launch_combine_backward(T, d, a.dy, a.y_saved, a.row_of, a.weights, w.dyo, dys, dg, true, s)
+                       : bwd::combine(T, d, a.dy, static_cast<const uint16_t *>(a.y_perm), a.row_of, a.weights, w.dyo,
+                                      dys, dg, true, s));
     CHK(q8_rows<true>(T, d, x, d, w.xq, w.xqs, s));
 
     FGemm base{};
@@ -709,10 +710,12 @@ hipError_t launch_backward_fp8(const BackwardArgs &a, void *ws, hipStream_t s) {
         CHK(kg(p, false));
     }
     // 7. router (fp32): dl and its share of dx, then the router gradient
-    CHK(bwd::router(T, d, x, a.w_router, a.idx, dg, w.dl, a.dx, s));
-    CHK(bwd::dwr(d, a.offsets, a.row_src, w.dl, x, w.dwr_part, a.dw_router, s));
+    if (a.w_router) {
+        CHK(bwd::router(T, d, x, a.w_router, a.idx, dg, w.dl, a.dx, s));
+        CHK(bwd::dwr(d, a.offsets, a.row_src, w.dl, x, w.dwr_part, a.dw_router, s));
+    }
     // 8. dx += shared + routed input gradients
-    CHK(bwd::dx(T, d, dxs, w.dxi, a.row_of, a.dx, s));
+    CHK(bwd::dx(T, d, dxs, w.dxi, a.row_of, a.dx, a.w_router != nullptr, s));
 #undef CHK
     return hipSuccess;
 }

@@ -1,0 +1,302 @@
+// Activation checkpoints in 8 bits, and the combine's gradient from them.
+//
+// A row is cut into tiles of 128 columns (the last may be shorter).  A tile has
+// one E8M0 scale 2^x, the smallest power of two at or above its largest
+// magnitude over the format's largest value (448 for e4m3, 127 for integers),
+// and a code per value: v / 2^x rounded to nearest even.  The quotient is exact,
+// so a code is off by half a step of its format and by nothing else: at most
+// 2^-4 of the value (e4m3, above its subnormals), 2^-7 of the tile's largest
+// (integers).  A tile that holds an infinity or a NaN gets scale byte 255, the
+// format's NaN, and reads back as NaN throughout: a lost activation shows.
+#include "device.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTile = 128;
+
+// The E8M0 byte of a tile: from the exponent of its largest magnitude, one more
+// where the mantissa is past the format's (448 = 1.75 * 2^8, 127 = 1.984375 *
+// 2^6).  At least 1 (2^-126), so the scale and its reciprocal are normal
+// numbers; 127 (scale 1) for an all-zero tile; 255 where a value is not finite.
+template <int FMT>
+__device__ __forceinline__ uint32_t tile_byte(uint32_t amax_bits) {
+    constexpr uint32_t kMant = FMT == kCkptE4M3 ? 0x600000u : 0x7e0000u;
+    constexpr int kShift = FMT == kCkptE4M3 ? 8 : 6;
+    if (amax_bits == 0) return 127u;
+    if (amax_bits >= 0x7f800000u) return 255u;
+    const int e = (int)(amax_bits >> 23) - kShift + ((amax_bits & 0x7fffffu) > kMant ? 1 : 0);
+    return (uint32_t)max(e, 1);
+}
+
+__device__ __forceinline__ float pow2_of_byte(uint32_t b) {
+    return b == 255u ? __uint_as_float(0x7fc00000u) : b == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
+}
+// 2^-x of a scale byte 1 .. 254.
+__device__ __forceinline__ float inverse_pow2(uint32_t b) {
+    return b == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - b) << 23);
+}
+
+// Four codes in one word.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    if (FMT == kCkptE4M3) return e4m3x4(a, b, c, d);
+    const uint32_t x = (uint32_t)(int)__builtin_rintf(a) & 0xffu, y = (uint32_t)(int)__builtin_rintf(b) & 0xffu,
+                   z = (uint32_t)(int)__builtin_rintf(c) & 0xffu, w = (uint32_t)(int)__builtin_rintf(d) & 0xffu;
+    return x | (y << 8) | (z << 16) | (w << 24);
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, float (&v)[4]) {
+    if (FMT == kCkptE4M3) {
+        const f32x2_hw lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+        const f32x2_hw hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+        v[0] = lo[0]; v[1] = lo[1]; v[2] = hi[0]; v[3] = hi[1];
+    } else {
+        v[0] = (float)(int8_t)(w & 0xffu); v[1] = (float)(int8_t)((w >> 8) & 0xffu);
+        v[2] = (float)(int8_t)((w >> 16) & 0xffu); v[3] = (float)(int8_t)(w >> 24);
+    }
+}
+
+// Eight consecutive values of a row (n of them inside it).
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const void *src, int64_t at, int n, float (&v)[8]) {
+    if (VEC && BF16) {
+        const i32x4 w = *reinterpret_cast<const i32x4 *>(static_cast<const uint16_t *>(src) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_to_f32((uint32_t)w[i] & 0xffffu);
+            v[2 * i + 1] = bf16_to_f32((uint32_t)w[i] >> 16);
+        }
+    } else if (VEC) {
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(src) + at);
+        const f32x4 b = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(src) + at + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = i >= n ? 0.f : BF16 ? bf16_to_f32(static_cast<const uint16_t *>(src)[at + i])
+                                       : static_cast<const float *>(src)[at + i];
+    }
+}
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store8(void *dst, int64_t at, int n, const float (&v)[8]) {
+    if (VEC && BF16) {
+        i32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (int)pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(dst) + at) = w;
+    } else if (VEC) {
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(dst) + at) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(dst) + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) {
+                if (BF16) static_cast<uint16_t *>(dst)[at + i] = (uint16_t)f32_to_bf16(v[i]);
+                else static_cast<float *>(dst)[at + i] = v[i];
+            }
+    }
+}
+
+// Sixteen lanes per tile, eight values each.
+template <bool BF16, int FMT, bool VEC>
+__global__ __launch_bounds__(256) void k_pack(int64_t rows, int cols, int ntile, const void *__restrict__ src, int64_t ld,
+                                              uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    const int sub = threadIdx.x & 15;
+    const int64_t tiles = rows * ntile, step = (int64_t)gridDim.x * 16;
+    for (int64_t base = (int64_t)blockIdx.x * 16; base < tiles; base += step) {
+        const int64_t tile = base + (threadIdx.x >> 4);
+        const bool on = tile < tiles;
+        const int64_t row = on ? tile / ntile : 0;
+        const int c = (int)(on ? tile - row * ntile : 0) * kTile + sub * 8;
+        const int n = on ? min(8, cols - c) : 0;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (n > 0) load8<BF16, VEC>(src, row * ld + c, n, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        for (int s = 8; s >= 1; s >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, s, kWave));
+        const uint32_t byte = tile_byte<FMT>(m);
+        if (!on) continue;
+        if (sub == 0) scales[tile] = (uint8_t)byte;
+        if (n <= 0) continue;
+        const float inv = byte == 255u ? 0.f : inverse_pow2(byte);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = byte == 255u ? 0.f : v[i] * inv;
+        const uint2 w = uint2{encode4<FMT>(v[0], v[1], v[2], v[3]), encode4<FMT>(v[4], v[5], v[6], v[7])};
+        if (VEC) {
+            *reinterpret_cast<uint2 *>(codes + row * cols + c) = w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) codes[row * cols + c + i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+        }
+    }
+}
+
+template <bool BF16, int FMT, bool VEC>
+__global__ __launch_bounds__(256) void k_unpack(int64_t rows, int cols, int ntile, const uint8_t *__restrict__ codes,
+                                                const uint8_t *__restrict__ scales, void *__restrict__ dst, int64_t ld) {
+    const int sub = threadIdx.x & 15;
+    const int64_t tiles = rows * ntile, step = (int64_t)gridDim.x * 16;
+    for (int64_t tile = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); tile < tiles; tile += step) {
+        const int64_t row = tile / ntile;
+        const int c = (int)(tile - row * ntile) * kTile + sub * 8;
+        const int n = min(8, cols - c);
+        if (n <= 0) continue;
+        const float scale = pow2_of_byte(scales[tile]);
+        uint2 w = uint2{0u, 0u};
+        if (VEC) {
+            w = *reinterpret_cast<const uint2 *>(codes + row * cols + c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) (i < 4 ? w.x : w.y) |= (uint32_t)codes[row * cols + c + i] << (8 * (i & 3));
+        }
+        float lo[4], hi[4], v[8];
+        decode4<FMT>(w.x, lo);
+        decode4<FMT>(w.y, hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[i] = lo[i] * scale; v[4 + i] = hi[i] * scale; }
+        store8<BF16, VEC>(dst, row * ld + c, n, v);
+    }
+}
+
+// ------------------------------------------------------- the combine's gradient
+
+template <bool F32>
+__device__ __forceinline__ void put8(void *base, int64_t at, const float (&v)[8]) {
+    store8<!F32, true>(base, at, 8, v);
+}
+
+// Eight consecutive saved values of row r at column c.
+template <int FMT>
+__device__ __forceinline__ void saved8(const Saved &y, int64_t r, int d, int ntile, int c, float (&v)[8]) {
+    if (FMT == kCkptBF16) {
+        load8<true, true>(y.data, r * d + c, 8, v);
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(y.data) + r * d + c);
+        const float scale = pow2_of_byte(y.scales[r * ntile + c / kTile]);
+        float lo[4], hi[4];
+        decode4<FMT>(w.x, lo);
+        decode4<FMT>(w.y, hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { v[i] = lo[i] * scale; v[4 + i] = hi[i] * scale; }
+    }
+}
+
+// One wave per token.  A row_of entry outside [0, T*8) is a choice that was not
+// dispatched: it has no row to write and its gradient is 0.
+template <int FMT, bool F32>
+__global__ __launch_bounds__(256) void k_combine_backward(int T, int d, int ntile, const float *__restrict__ dy, Saved y,
+                                                          const int32_t *__restrict__ row_of, const float *__restrict__ w,
+                                                          void *__restrict__ dyp, void *__restrict__ dys,
+                                                          float *__restrict__ dg) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T) return;
+    int r[8];
+    float g[8], dot[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        r[j] = row_of[t * 8 + j];
+        if (r[j] < 0 || (int64_t)r[j] >= (int64_t)T * 8) r[j] = -1;
+        g[j] = w[t * 8 + j];
+        dot[j] = 0.f;
+    }
+    for (int c = 8 * lane; c < d; c += 512) {
+        float v[8];
+        load8<false, true>(dy, t * d + c, 8, v);
+        if (dys) put8<F32>(dys, t * d + c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (r[j] < 0) continue;
+            float s[8], o[8];
+            saved8<FMT>(y, r[j], d, ntile, c, s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dot[j] += v[i] * s[i];
+                o[i] = g[j] * v[i];
+            }
+            put8<F32>(dyp, (int64_t)r[j] * d + c, o);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float v = dot[j];
+#pragma unroll
+        for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
+        if (lane == j) dg[t * 8 + j] = v;
+    }
+}
+
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether every eight columns can be read and written as whole vectors.
+bool vec_ok(const CkptArgs &a, const void *plain) {
+    return a.cols % 8 == 0 && a.ld % (a.bf16 ? 8 : 4) == 0 && aligned(plain, 16) && aligned(a.codes, 8);
+}
+
+unsigned tile_grid(int64_t tiles) {
+    const int64_t n = (tiles + 15) / 16;
+    return (unsigned)(n < (1 << 22) ? n : (1 << 22));
+}
+
+}  // namespace
+
+#define MOE_CKPT_VARIANTS(KERNEL, ...)                                                                    \
+    do {                                                                                                  \
+        if (a.format == kCkptE4M3) {                                                                      \
+            if (a.bf16 && vec) hipLaunchKernelGGL((KERNEL<true, kCkptE4M3, true>), __VA_ARGS__);          \
+            else if (a.bf16) hipLaunchKernelGGL((KERNEL<true, kCkptE4M3, false>), __VA_ARGS__);           \
+            else if (vec) hipLaunchKernelGGL((KERNEL<false, kCkptE4M3, true>), __VA_ARGS__);              \
+            else hipLaunchKernelGGL((KERNEL<false, kCkptE4M3, false>), __VA_ARGS__);                      \
+        } else {                                                                                          \
+            if (a.bf16 && vec) hipLaunchKernelGGL((KERNEL<true, kCkptI8, true>), __VA_ARGS__);            \
+            else if (a.bf16) hipLaunchKernelGGL((KERNEL<true, kCkptI8, false>), __VA_ARGS__);             \
+            else if (vec) hipLaunchKernelGGL((KERNEL<false, kCkptI8, true>), __VA_ARGS__);                \
+            else hipLaunchKernelGGL((KERNEL<false, kCkptI8, false>), __VA_ARGS__);                        \
+        }                                                                                                 \
+    } while (0)
+
+hipError_t launch_checkpoint_pack(const CkptArgs &a, hipStream_t s) {
+    const int ntile = (a.cols + kTile - 1) / kTile;
+    const bool vec = vec_ok(a, a.src);
+    const dim3 grid(tile_grid(a.rows * ntile)), block(256);
+    MOE_CKPT_VARIANTS(k_pack, grid, block, 0, s, a.rows, a.cols, ntile, a.src, a.ld, a.codes, a.scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s) {
+    const int ntile = (a.cols + kTile - 1) / kTile;
+    const bool vec = vec_ok(a, a.dst);
+    const dim3 grid(tile_grid(a.rows * ntile)), block(256);
+    MOE_CKPT_VARIANTS(k_unpack, grid, block, 0, s, a.rows, a.cols, ntile, a.codes, a.scales, a.dst, a.ld);
+    return hipGetLastError();
+}
+#undef MOE_CKPT_VARIANTS
+
+hipError_t launch_combine_backward(int T, int d, const float *dy, const Saved &y, const int32_t *row_of,
+                                   const float *weights, void *dyp, void *dys, float *dg, bool f32_out, hipStream_t s) {
+    const dim3 grid((unsigned)(((int64_t)T + 3) / 4)), block(256);
+    const int ntile = (d + kTile - 1) / kTile;
+#define GO(FMT)                                                                                                   \
+    do {                                                                                                          \
+        if (f32_out) hipLaunchKernelGGL((k_combine_backward<FMT, true>), grid, block, 0, s, T, d, ntile, dy, y,   \
+                                        row_of, weights, dyp, dys, dg);                                           \
+        else hipLaunchKernelGGL((k_combine_backward<FMT, false>), grid, block, 0, s, T, d, ntile, dy, y, row_of,  \
+                                weights, dyp, dys, dg);                                                           \
+    } while (0)
+    if (y.format == kCkptE4M3) GO(kCkptE4M3);
+    else if (y.format == kCkptI8) GO(kCkptI8);
+    else GO(kCkptBF16);
+#undef GO
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -9,6 +9,13 @@ namespace moe {
 
 enum Dtype { kF32 = 0, kBF16 = 1, kE4M3 = 2 };
 
+enum CkptFormat { kCkptBF16 = 0, kCkptE4M3 = 1, kCkptI8 = 2 };
+// A saved activation: bf16 values, or 8-bit codes with their tiles' scales.
+struct Saved {
+    const void *data;
+    const uint8_t *scales;
+    int format;
+};
 struct RouteArgs {
     int T, d;
     bool x_bf16;
@@ -184,6 +191,98 @@ hipError_t launch_fp8_mx_gemm(const Fp8GemmArgs &g, hipStream_t s);
 bool fp8_mx_kg_ok(const Fp8KgArgs &g);
 hipError_t launch_fp8_mx_kg(const Fp8KgArgs &g, hipStream_t s);
 
+// Expert choice from logits (csrc/select.hip).
+struct SelectRule {
+    int E, k;
+    bool softmax;
+    int n_group, topk_group;
+    bool top_two;  // group score: sum of the two best, else the best
+    bool renorm;
+    float scale;
+};
+struct SelectArgs {
+    SelectRule rule;
+    int T;
+    bool bf16;           // type of the logits
+    const void *logits;  // [T, E], rows ld elements apart
+    int64_t ld;
+    const float *bias;   // [E] or nullptr
+    int32_t *idx;
+    float *weights;
+};
+constexpr int kSelectMaxE = 1024, kSelectMaxK = 64;
+hipError_t launch_select(const SelectArgs &a, hipStream_t s);
+// The balance loss's share of the gradient (seq == nullptr: none).
+struct BalanceGrad {
+    const int32_t *seq;  // [n_seq + 1]
+    int n_seq;
+    const float *load, *dloss;
+    float alpha;
+};
+struct SelectBackwardArgs {
+    SelectRule rule;
+    int T;
+    bool bf16;
+    const void *logits;
+    int64_t ld;
+    const int32_t *idx;
+    const float *dweights;  // nullptr: no gradient through the weights
+    BalanceGrad balance;
+    float *dlogits;
+};
+hipError_t launch_select_backward(const SelectBackwardArgs &a, hipStream_t s);
+constexpr int kBalanceTokens = 64;  // tokens per workgroup of the loss's partial sums
+struct BalanceArgs {
+    SelectRule rule;  // E, k and softmax are read
+    int T;
+    bool bf16;
+    const void *logits;
+    int64_t ld;
+    const int32_t *idx, *seq;
+    int n_seq;
+    float alpha;
+    float *loss, *load;
+};
+size_t balance_ws_bytes(int T, int E, int n_seq);
+hipError_t launch_balance_loss(const BalanceArgs &a, void *ws, hipStream_t s);
+
+// 8-bit activation checkpoints (csrc/checkpoint.hip): rows in 1x128 tiles with
+// an E8M0 scale each, codes e4m3 or int8.
+struct CkptArgs {
+    int64_t rows;
+    int cols;
+    bool bf16;       // type of the plain side
+    int format;      // kCkptE4M3 or kCkptI8
+    const void *src; // pack: the values; unpack: nullptr
+    void *dst;       // unpack: the values; pack: nullptr
+    int64_t ld;      // elements between rows of the plain side
+    uint8_t *codes, *scales;
+};
+hipError_t launch_checkpoint_pack(const CkptArgs &a, hipStream_t s);
+hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s);
+
+// dg[t, j] = dy[t] . y[row_of[t*8 + j]]; dyp row row_of[t*8 + j] = weights[t, j]
+// dy[t]; dys (nullptr: not written) row t = dy[t]; both bf16, or fp32 when
+// f32_out.  d a multiple of 64.
+hipError_t launch_combine_backward(int T, int d, const float *dy, const Saved &y, const int32_t *row_of,
+                                   const float *weights, void *dyp, void *dys, float *dg, bool f32_out, hipStream_t s);
+
+// Router projection from the logits' side (csrc/router_grad.hip): dx = dx_in +
+// dlogits w, dw = dlogits^T x, E = 256.
+struct RouterGradArgs {
+    int T, d;
+    bool x_bf16;
+    const void *x;
+    const float *w, *dlogits, *dx_in;  // dx_in nullptr: zero
+    float *dx, *dw;
+};
+size_t router_grad_ws_bytes(int T, int d, bool x_bf16);
+hipError_t launch_router_grad(const RouterGradArgs &a, void *ws, hipStream_t s);
+// logits[T, 256] = x w^T of the router, by the kernels of moe_route.
+hipError_t launch_router_logits_f32(int T, int d, const float *x, const float *wr, float *logits, hipStream_t s);
+hipError_t launch_router_logits_bf16(int T, int d, const void *x, const float *wr, float *logits, void *ws,
+                                     hipStream_t s);
+
 hipError_t launch_bias_update(int E, int k, int T, const int32_t *counts, float gamma, float *bias,
                               hipStream_t s);
 
@@ -191,7 +290,7 @@ hipError_t launch_bias_update(int E, int k, int T, const int32_t *counts, float 
 struct BackwardArgs {
     int T, d, I, k;
     const void *x;            // [T, d] bf16
-    const float *w_router;    // [E, d]
+    const float *w_router;    // [E, d], or nullptr: no router share (dx the experts' alone, dw_router not written)
     const int32_t *idx;       // [T, k] chosen ids (ascending)
     const float *weights;     // [T, k] combine weights
     const int32_t *offsets, *row_src, *row_of;
@@ -200,6 +299,8 @@ struct BackwardArgs {
     const float *dy;          // [T, d]
     float *dx, *dw_router, *dw_gate, *dw_up, *dw_down, *ds_gate, *ds_up, *ds_down;
     float *dg;                // [T, k] or nullptr
+    // y_perm instead from a checkpoint when y_saved.data is not null
+    Saved y_saved{};
 };
 size_t backward_ws_bytes(int T, int d, int I, int k);
 bool backward_ok(int d, int I);

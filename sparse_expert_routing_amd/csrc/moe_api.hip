@@ -82,6 +82,56 @@ size_t combine_ws(const moe_desc_t *d) {
            align_up(moe::ffn_shared_split_bytes(d->T, d->d, d->I, d->wt));
 }
 
+// The saved-activation backward: x unpacked to bf16, then the backward's own.
+size_t saved_x_bytes(const moe_desc_t *d) { return align_up((size_t)d->T * d->d * 2); }
+size_t backward_saved_ws(const moe_desc_t *d) {
+    const size_t b = backward_ws(d);
+    return b ? saved_x_bytes(d) + b : 0;
+}
+
+size_t router_grad_ws(const moe_desc_t *d) {
+    return align_up(moe::router_grad_ws_bytes(d->T, d->d, d->act == MOE_BF16));
+}
+
+moe_status_t check_select(const moe_select_t *s) {
+    if (s == nullptr) return MOE_EINVAL;
+    if (s->T <= 0 || s->E <= 0 || s->k <= 0 || s->k > s->E) return MOE_EINVAL;
+    if (s->score != MOE_SIGMOID && s->score != MOE_SOFTMAX) return MOE_EINVAL;
+    if (s->n_group <= 0 || s->topk_group <= 0 || s->topk_group > s->n_group || s->E % s->n_group != 0) return MOE_EINVAL;
+    if ((int64_t)s->topk_group * (s->E / s->n_group) < s->k) return MOE_EINVAL;
+    if (s->group_score != MOE_GROUP_MAX && s->group_score != MOE_GROUP_TOP_TWO) return MOE_EINVAL;
+    if (s->renorm != 0 && s->renorm != 1) return MOE_EINVAL;
+    if (!(s->scale - s->scale == 0.f)) return MOE_EINVAL;  // infinite or NaN
+    if (s->logits != MOE_F32 && s->logits != MOE_BF16) return s->logits == MOE_E4M3 ? MOE_ENOTSUP : MOE_EINVAL;
+    if (s->E > moe::kSelectMaxE || s->k > moe::kSelectMaxK) return MOE_ENOTSUP;
+    if ((int64_t)s->T * s->k >= (1LL << 31)) return MOE_ENOTSUP;
+    return MOE_OK;
+}
+
+moe::SelectRule rule_of(const moe_select_t *s) {
+    return moe::SelectRule{s->E, s->k, s->score == MOE_SOFTMAX, s->n_group, s->topk_group,
+                           s->group_score == MOE_GROUP_TOP_TWO, s->renorm == 1, s->scale};
+}
+
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+bool saved_ok(const moe_saved_t *s) {
+    if (s == nullptr || s->data == nullptr || !aligned16(s->data)) return false;
+    if (s->format == MOE_SAVED_BF16) return true;
+    return (s->format == MOE_SAVED_E4M3 || s->format == MOE_SAVED_I8) && s->scales != nullptr;
+}
+
+moe::Saved to_internal(const moe_saved_t *s) { return moe::Saved{s->data, s->scales, s->format}; }
+
+moe_status_t check_checkpoint(int64_t rows, int32_t cols, int32_t type, int64_t ld, int32_t format) {
+    if (rows <= 0 || cols <= 0 || ld < cols) return MOE_EINVAL;
+    if (type != MOE_F32 && type != MOE_BF16) return type == MOE_E4M3 ? MOE_ENOTSUP : MOE_EINVAL;
+    if (format != MOE_SAVED_E4M3 && format != MOE_SAVED_I8) return MOE_EINVAL;
+    // byte offsets in 63 bits
+    if (rows > INT64_MAX / 4 / ld) return MOE_ENOTSUP;
+    return MOE_OK;
+}
+
 moe_status_t hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
 bool ffn_weights_ok(const moe_ffn_weights_t *w, int wt) {
@@ -118,6 +168,9 @@ size_t moe_workspace_bytes(const moe_desc_t *d, int32_t stage) {
         case MOE_WS_FFN: return routed_ffn_ws(d);
         case MOE_WS_COMBINE: return combine_ws(d);
         case MOE_WS_BACKWARD: return backward_ws(d);
+        case MOE_WS_ROUTER_LOGITS: return route_ws(d);
+        case MOE_WS_ROUTER_GRAD: return router_grad_ws(d);
+        case MOE_WS_BACKWARD_SAVED: return backward_saved_ws(d);
     }
     return 0;
 }
@@ -307,6 +360,52 @@ moe_status_t moe_bias_update(const moe_desc_t *d, const int32_t *counts, float g
                                               static_cast<hipStream_t>(stream)));
 }
 
+// moe_backward and moe_backward_saved: x and y_perm in bf16 or as 8-bit
+// checkpoints (ws_x: room for x in bf16, at the front of the workspace).
+static moe_status_t backward_of(const moe_desc_t *d, const moe_saved_t *x, const float *w_router, const int32_t *idx,
+                                const float *weights, const int32_t *offsets, const int32_t *row_src,
+                                const int32_t *row_of, const moe_ffn_weights_t *experts,
+                                const moe_ffn_weights_t *shared, const moe_saved_t *y_perm, const float *dy, float *dx,
+                                float *dw_router, float *dw_gate, float *dw_up, float *dw_down, float *ds_gate,
+                                float *ds_up, float *ds_down, float *dg, void *workspace, size_t ws_x, void *stream) {
+    char *ws = static_cast<char *>(workspace);
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    moe::BackwardArgs a{};
+    a.x = x->data;
+    if (x->format != MOE_SAVED_BF16) {
+        const moe::CkptArgs c{d->T, d->d, true, x->format, nullptr, ws, d->d,
+                              static_cast<uint8_t *>(const_cast<void *>(x->data)), const_cast<uint8_t *>(x->scales)};
+        if (moe::launch_checkpoint_unpack(c, hs) != hipSuccess) return MOE_EHIP;
+        a.x = ws;
+    }
+    ws += ws_x;
+    a.T = d->T;
+    a.d = d->d;
+    a.I = d->I;
+    a.k = d->k;
+    a.w_router = w_router;
+    a.idx = idx;
+    a.weights = weights;
+    a.offsets = offsets;
+    a.row_src = row_src;
+    a.row_of = row_of;
+    a.experts = to_internal(experts);
+    a.shared = to_internal(shared);
+    a.y_perm = y_perm->data;
+    if (y_perm->format != MOE_SAVED_BF16) a.y_saved = to_internal(y_perm);
+    a.dy = dy;
+    a.dx = dx;
+    a.dw_router = dw_router;
+    a.dw_gate = dw_gate;
+    a.dw_up = dw_up;
+    a.dw_down = dw_down;
+    a.ds_gate = ds_gate;
+    a.ds_up = ds_up;
+    a.ds_down = ds_down;
+    a.dg = dg;
+    return hip_status(d->wt == MOE_E4M3 ? moe::launch_backward_fp8(a, ws, hs) : moe::launch_backward(a, ws, hs));
+}
+
 moe_status_t moe_backward(const moe_desc_t *d, const void *x, const float *w_router, const int32_t *idx,
                           const float *weights, const int32_t *offsets, const int32_t *row_src,
                           const int32_t *row_of, const moe_ffn_weights_t *experts,
@@ -323,34 +422,121 @@ moe_status_t moe_backward(const moe_desc_t *d, const void *x, const float *w_rou
         !ffn_weights_ok(experts, d->wt) || !ffn_weights_ok(shared, d->wt))
         return MOE_EINVAL;
     if (!workspace || ws_bytes < backward_ws(d)) return MOE_EWORKSPACE;
-    moe::BackwardArgs a{};
-    a.T = d->T;
-    a.d = d->d;
-    a.I = d->I;
-    a.k = d->k;
-    a.x = x;
-    a.w_router = w_router;
-    a.idx = idx;
-    a.weights = weights;
-    a.offsets = offsets;
-    a.row_src = row_src;
-    a.row_of = row_of;
-    a.experts = to_internal(experts);
-    a.shared = to_internal(shared);
-    a.y_perm = y_perm;
-    a.dy = dy;
-    a.dx = dx;
-    a.dw_router = dw_router;
-    a.dw_gate = dw_gate;
-    a.dw_up = dw_up;
-    a.dw_down = dw_down;
-    a.ds_gate = ds_gate;
-    a.ds_up = ds_up;
-    a.ds_down = ds_down;
-    a.dg = dg;
-    const hipStream_t hs = static_cast<hipStream_t>(stream);
-    return hip_status(d->wt == MOE_E4M3 ? moe::launch_backward_fp8(a, workspace, hs)
-                                        : moe::launch_backward(a, workspace, hs));
+    const moe_saved_t xs{x, nullptr, MOE_SAVED_BF16}, ys{y_perm, nullptr, MOE_SAVED_BF16};
+    return backward_of(d, &xs, w_router, idx, weights, offsets, row_src, row_of, experts, shared, &ys, dy, dx, dw_router,
+                       dw_gate, dw_up, dw_down, ds_gate, ds_up, ds_down, dg, workspace, 0, stream);
+}
+
+moe_status_t moe_backward_saved(const moe_desc_t *d, const moe_saved_t *x, const float *w_router, const int32_t *idx,
+                                const float *weights, const int32_t *offsets, const int32_t *row_src,
+                                const int32_t *row_of, const moe_ffn_weights_t *experts,
+                                const moe_ffn_weights_t *shared, const moe_saved_t *y_perm, const float *dy, float *dx,
+                                float *dw_router, float *dw_gate, float *dw_up, float *dw_down, float *ds_gate,
+                                float *ds_up, float *ds_down, float *dg, void *workspace, size_t ws_bytes,
+                                void *stream) {
+    moe_status_t st = check_desc(d);
+    if (st != MOE_OK) return st;
+    if (d->act != MOE_BF16 || (d->wt != MOE_BF16 && d->wt != MOE_E4M3) || !moe::backward_ok(d->d, d->I))
+        return MOE_ENOTSUP;
+    if (!weights || !offsets || !row_src || !row_of || !dy || !dx || !dw_gate || !dw_up || !dw_down || !ds_gate ||
+        !ds_up || !ds_down || !saved_ok(x) || !saved_ok(y_perm) || !ffn_weights_ok(experts, d->wt) ||
+        !ffn_weights_ok(shared, d->wt))
+        return MOE_EINVAL;
+    if (w_router ? (!dw_router || !idx) : (dw_router || !dg)) return MOE_EINVAL;
+    if (!workspace || ws_bytes < backward_saved_ws(d)) return MOE_EWORKSPACE;
+    return backward_of(d, x, w_router, idx, weights, offsets, row_src, row_of, experts, shared, y_perm, dy, dx, dw_router,
+                       dw_gate, dw_up, dw_down, ds_gate, ds_up, ds_down, dg, workspace, saved_x_bytes(d), stream);
+}
+
+moe_status_t moe_combine_backward(const moe_desc_t *d, const float *dy, const moe_saved_t *y_perm,
+                                  const int32_t *row_of, const float *weights, void *dy_perm, float *dg, void *stream) {
+    moe_status_t st = check_desc(d);
+    if (st != MOE_OK) return st;
+    if (!dy || !row_of || !weights || !dy_perm || !dg || !saved_ok(y_perm)) return MOE_EINVAL;
+    if (!aligned16(dy) || !aligned16(dy_perm)) return MOE_EINVAL;
+    return hip_status(moe::launch_combine_backward(d->T, d->d, dy, to_internal(y_perm), row_of, weights, dy_perm, nullptr,
+                                                   dg, false, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_checkpoint_pack(int64_t rows, int32_t cols, int32_t type, const void *src, int64_t ld, int32_t format,
+                                 uint8_t *codes, uint8_t *scales, void *stream) {
+    moe_status_t st = check_checkpoint(rows, cols, type, ld, format);
+    if (st != MOE_OK) return st;
+    if (!src || !codes || !scales) return MOE_EINVAL;
+    const moe::CkptArgs a{rows, cols, type == MOE_BF16, format, src, nullptr, ld, codes, scales};
+    return hip_status(moe::launch_checkpoint_pack(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_checkpoint_unpack(int64_t rows, int32_t cols, int32_t type, const uint8_t *codes,
+                                   const uint8_t *scales, int32_t format, void *dst, int64_t ld, void *stream) {
+    moe_status_t st = check_checkpoint(rows, cols, type, ld, format);
+    if (st != MOE_OK) return st;
+    if (!dst || !codes || !scales) return MOE_EINVAL;
+    const moe::CkptArgs a{rows, cols, type == MOE_BF16, format, nullptr, dst, ld, const_cast<uint8_t *>(codes),
+                          const_cast<uint8_t *>(scales)};
+    return hip_status(moe::launch_checkpoint_unpack(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_router_logits(const moe_desc_t *d, const void *x, const float *w_router, float *logits,
+                               void *workspace, size_t ws_bytes, void *stream) {
+    moe_status_t st = check_desc(d);
+    if (st != MOE_OK) return st;
+    if (!x || !w_router || !logits) return MOE_EINVAL;
+    const size_t need = route_ws(d);
+    if (need && (!workspace || ws_bytes < need)) return MOE_EWORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (need) return hip_status(moe::launch_router_logits_bf16(d->T, d->d, x, w_router, logits, workspace, s));
+    return hip_status(moe::launch_router_logits_f32(d->T, d->d, static_cast<const float *>(x), w_router, logits, s));
+}
+
+moe_status_t moe_router_logits_backward(const moe_desc_t *d, const void *x, const float *w_router,
+                                        const float *dlogits, const float *dx_in, float *dx, float *dw_router,
+                                        void *workspace, size_t ws_bytes, void *stream) {
+    moe_status_t st = check_desc(d);
+    if (st != MOE_OK) return st;
+    if (!x || !w_router || !dlogits || !dx || !dw_router) return MOE_EINVAL;
+    const size_t need = router_grad_ws(d);
+    if (need && (!workspace || ws_bytes < need)) return MOE_EWORKSPACE;
+    const moe::RouterGradArgs a{d->T, d->d, d->act == MOE_BF16, x, w_router, dlogits, dx_in, dx, dw_router};
+    return hip_status(moe::launch_router_grad(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_select(const moe_select_t *sel, const void *logits, int64_t ld, const float *bias, int32_t *idx,
+                        float *weights, void *stream) {
+    moe_status_t st = check_select(sel);
+    if (st != MOE_OK) return st;
+    if (!logits || !idx || !weights || ld < sel->E) return MOE_EINVAL;
+    const moe::SelectArgs a{rule_of(sel), sel->T, sel->logits == MOE_BF16, logits, ld, bias, idx, weights};
+    return hip_status(moe::launch_select(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_select_backward(const moe_select_t *sel, const void *logits, int64_t ld, const int32_t *idx,
+                                 const float *dweights, const int32_t *seq_offsets, int32_t n_seq, const float *load,
+                                 const float *dloss, float alpha, float *dlogits, void *stream) {
+    moe_status_t st = check_select(sel);
+    if (st != MOE_OK) return st;
+    if (!logits || !dlogits || ld < sel->E || (!dweights && !seq_offsets) || (dweights && !idx)) return MOE_EINVAL;
+    if (seq_offsets && (!load || !dloss || n_seq <= 0)) return MOE_EINVAL;
+    const moe::SelectBackwardArgs a{rule_of(sel), sel->T, sel->logits == MOE_BF16, logits, ld, idx, dweights,
+                                    moe::BalanceGrad{seq_offsets, n_seq, load, dloss, alpha}, dlogits};
+    return hip_status(moe::launch_select_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_balance_workspace_bytes(const moe_select_t *sel, int32_t n_seq) {
+    if (check_select(sel) != MOE_OK || n_seq <= 0) return 0;
+    return align_up(moe::balance_ws_bytes(sel->T, sel->E, n_seq));
+}
+
+moe_status_t moe_balance_loss(const moe_select_t *sel, const void *logits, int64_t ld, const int32_t *idx,
+                              const int32_t *seq_offsets, int32_t n_seq, float alpha, float *loss, float *load,
+                              void *workspace, size_t ws_bytes, void *stream) {
+    moe_status_t st = check_select(sel);
+    if (st != MOE_OK) return st;
+    if (!logits || !idx || !seq_offsets || !loss || !load || n_seq <= 0 || ld < sel->E) return MOE_EINVAL;
+    if (!workspace || ws_bytes < moe_balance_workspace_bytes(sel, n_seq)) return MOE_EWORKSPACE;
+    const moe::BalanceArgs a{rule_of(sel), sel->T, sel->logits == MOE_BF16, logits, ld, idx, seq_offsets, n_seq, alpha,
+                             loss, load};
+    return hip_status(moe::launch_balance_loss(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -34,7 +34,8 @@ constexpr int kXPad = 4;
 constexpr int kSPad = 4;
 constexpr int kChunk = 512;  // K between flushes of the partial accumulators
 
-template <bool kXBf16, int kK>
+// kLogits: the logits themselves go to wts [T, 256] and nothing is chosen.
+template <bool kXBf16, int kK, bool kLogits = false>
 __global__ __launch_bounds__(256) void k_route(int T, int d, const void *__restrict__ x,
                                                const float *__restrict__ wr,
                                                const float *__restrict__ bias,
@@ -120,6 +121,18 @@ __global__ __launch_bounds__(256) void k_route(int T, int d, const void *__restr
 
     // C layout of a 16x16 MFMA tile: lane holds column (lane & 15) and rows
     // 4 * (lane >> 4) + r.
+    if (kLogits) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = t0 + 16 * i + 4 * (lane >> 4) + r;
+                    if (t < T) wts[(size_t)t * kE + n0 + 16 * j + (lane & 15)] = tot[i][j][r];
+                }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -196,6 +209,12 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t s) {
         hipLaunchKernelGGL((k_route<true, 8>), grid, block, 0, s, a.T, a.d, a.x, a.wr, a.bias, a.idx, a.w, a.gap);
     else
         hipLaunchKernelGGL((k_route<false, 8>), grid, block, 0, s, a.T, a.d, a.x, a.wr, a.bias, a.idx, a.w, a.gap);
+    return hipGetLastError();
+}
+
+hipError_t launch_router_logits_f32(int T, int d, const float *x, const float *wr, float *logits, hipStream_t s) {
+    hipLaunchKernelGGL((k_route<false, 8, true>), dim3((T + kTok - 1) / kTok), dim3(256), 0, s, T, d, x, wr, nullptr,
+                       nullptr, logits, nullptr);
     return hipGetLastError();
 }
 

@@ -247,6 +247,17 @@ __global__ __launch_bounds__(256) void k_route_topk(int T, int S, const float *_
         gap[t] = f32_from_order_key((uint32_t)(kth >> 32)) - f32_from_order_key((uint32_t)(k1th >> 32));
 }
 
+// logits = the S partial logits added in split order (4 per thread).
+__global__ __launch_bounds__(256) void k_logits_sum(int64_t n4, int S, const f32x4 *__restrict__ part,
+                                                    f32x4 *__restrict__ logits) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    f32x4 v = part[i];
+#pragma unroll 4
+    for (int z = 1; z < S; ++z) v += part[(int64_t)z * n4 + i];
+    logits[i] = v;
+}
+
 }  // namespace
 
 // K splits of the logits GEMM: up to about 256 workgroups for small T, each
@@ -277,6 +288,25 @@ hipError_t launch_route_bf16(const RouteArgs &a, void *ws, hipStream_t s) {
                        static_cast<const uint16_t *>(a.x), wsplit, logits);
     hipLaunchKernelGGL((k_route_topk<8>), dim3((a.T + 3) / 4), dim3(256), 0, s, a.T, S, logits, a.bias, a.idx,
                        a.w, a.gap);
+    return hipGetLastError();
+}
+
+hipError_t launch_router_logits_bf16(int T, int d, const void *x, const float *wr, float *logits, void *ws,
+                                     hipStream_t s) {
+    uint16_t *wsplit = static_cast<uint16_t *>(ws);
+    const size_t split = ((size_t)3 * kE * d * sizeof(uint16_t) + 255) / 256 * 256;
+    float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + split);
+    const int n = kE * d, S = route_ksplit(T, d);
+    hipLaunchKernelGGL(k_router_split, dim3((n + 255) / 256), dim3(256), 0, s, n, wr, wsplit, wsplit + n,
+                       wsplit + 2 * (size_t)n);
+    // one split: its partial logits are the logits
+    hipLaunchKernelGGL(k_router_logits, dim3((T + RM - 1) / RM, kE / RN, S), dim3(256), 0, s, T, d,
+                       static_cast<const uint16_t *>(x), wsplit, S == 1 ? logits : part);
+    if (S > 1) {
+        const int64_t n4 = (int64_t)T * kE / 4;
+        hipLaunchKernelGGL(k_logits_sum, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, n4, S,
+                           reinterpret_cast<const f32x4 *>(part), reinterpret_cast<f32x4 *>(logits));
+    }
     return hipGetLastError();
 }
 

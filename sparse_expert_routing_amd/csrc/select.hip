@@ -1,0 +1,477 @@
+// Expert choice from router logits, its gradient, and the sequence-wise balance
+// loss.
+//
+// One wave per token; lane l holds the experts l, l + 64, ... of the row.
+//   scores   s = sigmoid(l) or softmax(l) over the row
+//   choice   a = s + bias (the bias steers the choice only); the experts are
+//            cut into groups, the best groups by max or top-two sum of a stay
+//            open, the k largest a inside them are chosen; ties to the lower id
+//   weights  scale * s_j, over the chosen scores' sum when renormalised
+// The choice is that of 64-bit scores: it decides whole numbers, and an fp32
+// score's rounding would decide them differently from one exp to the next.
+// Without a bias the order of the scores is the order of the logits, so the
+// logits themselves are compared and nothing is rounded.
+#include "device.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+// Totally ordered key of a double (larger value -> larger key); 1 for a NaN,
+// which ranks below every number, and never 0, which marks an expert that
+// cannot be chosen.  -0 and +0 get the same key.
+__device__ __forceinline__ uint64_t f64_order_key(double v) {
+    if (v != v) return 1;
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double f64_from_order_key(uint64_t k) {
+    return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
+}
+
+__device__ __forceinline__ float wave_sum_f32(float v) {
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
+    return v;
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
+    return v;
+}
+
+// Orders a wave's own LDS stores before its lanes' loads of each other's values.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void *row, int e) {
+    return BF16 ? bf16_to_f32(static_cast<const uint16_t *>(row)[e]) : static_cast<const float *>(row)[e];
+}
+
+__device__ __forceinline__ float sigmoid_f32(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// e^(l - m) of a softmax whose maximum is m; a row of -inf has no mass at all.
+__device__ __forceinline__ float softmax_term(float l, float m) { return m == -INFINITY ? 0.f : expf(l - m); }
+
+// The n largest of the keys of a wave (key[q] of lane l: item l + 64 q; 0 = no
+// item), as a bit mask over q in each lane; equal keys go to the lower item.
+template <int Q>
+__device__ __forceinline__ uint32_t wave_top(uint64_t (&key)[Q], int n) {
+    const int lane = threadIdx.x & 63;
+    uint32_t chosen = 0;
+    for (int r = 0; r < n; ++r) {
+        uint64_t m = key[0];
+#pragma unroll
+        for (int q = 1; q < Q; ++q) m = key[q] > m ? key[q] : m;
+        m = wave_max_u64(m);
+        bool open = m != 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const uint64_t at = __ballot(key[q] == m);
+            if (open && at != 0) {
+                open = false;
+                if (lane == __ffsll((unsigned long long)at) - 1) {
+                    chosen |= 1u << q;
+                    key[q] = 0;
+                }
+            }
+        }
+    }
+    return chosen;
+}
+
+// The choice for one token in 64 bits: the chosen experts as a bit mask over q
+// in each lane (expert lane + 64 q).  score64: this wave's E doubles in LDS,
+// open: its group flags.
+template <int Q>
+__device__ __forceinline__ uint32_t choose64(const SelectRule &r, const float (&l)[Q], const float *__restrict__ bias,
+                                             double *score64, uint8_t *open) {
+    const int lane = threadIdx.x & 63;
+    double s[Q];
+    if (r.softmax) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) m = fmaxf(m, l[q]);
+        m = wave_max_f32(m, kWave);
+        double sum = 0.0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            s[q] = lane + 64 * q < r.E && m != -INFINITY ? exp((double)l[q] - (double)m) : 0.0;
+            sum += s[q];
+        }
+        sum = wave_sum_f64(sum);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) s[q] = m == -INFINITY ? 0.0 : s[q] / sum;
+    } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) s[q] = 1.0 / (1.0 + exp(-(double)l[q]));
+    }
+    uint64_t key[Q];
+    double a[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int e = lane + 64 * q;
+        a[q] = bias && e < r.E ? s[q] + (double)bias[e] : s[q];
+        key[q] = e < r.E ? f64_order_key(bias ? a[q] : (double)l[q]) : 0;
+    }
+    if (r.topk_group < r.n_group) {
+        const int per = r.E / r.n_group;
+        // without a bias, the best of a group is that of its logits
+        const bool by_logit = !bias && !r.top_two;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (lane + 64 * q < r.E) score64[lane + 64 * q] = by_logit ? (double)l[q] : a[q];
+        wave_sync();
+        uint64_t gkey[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int g = lane + 64 * q;
+            gkey[q] = 0;
+            if (g >= r.n_group) continue;
+            uint64_t k1 = 0, k2 = 0;
+            for (int i = 0; i < per; ++i) {
+                const uint64_t k = f64_order_key(score64[g * per + i]);
+                k2 = k > k1 ? k1 : (k > k2 ? k : k2);
+                k1 = k > k1 ? k : k1;
+            }
+            if (r.top_two && k1 > 1 && k2 > 1)
+                k1 = f64_order_key(f64_from_order_key(k1) + f64_from_order_key(k2));
+            else if (r.top_two && per > 1)
+                k1 = 1;  // fewer than two numbers: behind every group that has two
+            gkey[q] = k1;
+        }
+        const uint32_t go = wave_top<Q>(gkey, r.topk_group);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (lane + 64 * q < r.n_group) open[lane + 64 * q] = (go >> q) & 1;
+        wave_sync();
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (key[q] != 0 && !open[(lane + 64 * q) / per]) key[q] = 0;
+    }
+    return wave_top<Q>(key, r.k);
+}
+
+// The chosen ids in ascending order and their weights.
+template <int Q>
+__device__ __forceinline__ void store_choice(const SelectRule &r, int64_t t, uint32_t chosen, const float (&l)[Q],
+                                             int32_t *__restrict__ idx, float *__restrict__ wts) {
+    const int lane = threadIdx.x & 63;
+    float s[Q], total;
+    if (r.softmax) {
+        // relative to the largest logit that the denominator has
+        float m = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (!r.renorm || ((chosen >> q) & 1)) m = fmaxf(m, l[q]);
+        m = wave_max_f32(m, kWave);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            s[q] = softmax_term(l[q], m);
+            if (lane + 64 * q < r.E && (!r.renorm || ((chosen >> q) & 1))) sum += s[q];
+        }
+        total = wave_sum_f32(sum);
+    } else {
+        float sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            s[q] = sigmoid_f32(l[q]);
+            if ((chosen >> q) & 1) sum += s[q];
+        }
+        total = r.renorm ? wave_sum_f32(sum) : 1.f;
+    }
+    int base = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const bool mine = (chosen >> q) & 1;
+        const uint64_t at = __ballot(mine);
+        if (mine) {
+            const int64_t o = t * r.k + base + __popcll(at & ((1ull << lane) - 1));
+            idx[o] = lane + 64 * q;
+            wts[o] = total == 0.f ? 0.f : r.scale * (s[q] / total);
+        }
+        base += __popcll(at);
+    }
+}
+
+template <int Q, bool BF16>
+__global__ __launch_bounds__(256) void k_select(SelectRule r, int T, const void *__restrict__ logits, int64_t ld,
+                                                const float *__restrict__ bias, int32_t *__restrict__ idx,
+                                                float *__restrict__ wts) {
+    __shared__ double score64[4][64 * Q];
+    __shared__ uint8_t open[4][64 * Q];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    if (t >= T) return;
+    const void *row = static_cast<const char *>(logits) + t * ld * (BF16 ? 2 : 4);
+    float l[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) l[q] = lane + 64 * q < r.E ? load_logit<BF16>(row, lane + 64 * q) : -INFINITY;
+    const uint32_t chosen = choose64<Q>(r, l, bias, score64[wave], open[wave]);
+    store_choice<Q>(r, t, chosen, l, idx, wts);
+}
+
+// ------------------------------------------------------------- the sequences
+
+// How many of the sequences [0, n) end at or before token t (their ends are
+// ascending): the sequence that holds t, or n behind the last one.  Sixty-four
+// ends are compared at a time.
+__device__ __forceinline__ int sequence_of(const int32_t *__restrict__ off, int n, int t) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0;
+    while (n > 64) {
+        const int step = (n + 63) / 64;
+        const int i = min(lane * step + step, n) - 1;
+        const int full = __popcll(__ballot(off[1 + lo + i] <= t));
+        if (full == 64) return lo + n;
+        lo += full * step;
+        n = min(step, n - full * step);
+        if (n <= 0) return lo;
+    }
+    return lo + __popcll(__ballot(lane < n && off[1 + lo + min(lane, n - 1)] <= t));
+}
+
+// The gradient with respect to the logits of one token:
+//   weights, renormalised: r_j (c dw_j - sum_i c dw_i r_i) with r the chosen
+//     shares, times (1 - s_j) for a sigmoid; as they are: sigmoid c dw_j s_j
+//     (1 - s_j), softmax p_e (c dw_e - sum_j c dw_j p_j) over all experts;
+//   balance: p'_e (b_e - sum_i b_i p'_i), times (1 - s_e) for a sigmoid, with p'
+//     the scores over their sum and b_e = alpha dloss load_e / tokens.
+// Written in the shares r and p' (never in ds / S), nothing overflows where a
+// row's scores are tiny; a row with no score at all has no gradient.
+template <int Q, bool BF16>
+__global__ __launch_bounds__(256) void k_select_backward(SelectRule r, int T, const void *__restrict__ logits,
+                                                         int64_t ld, const int32_t *__restrict__ idx,
+                                                         const float *__restrict__ dw, BalanceGrad b,
+                                                         float *__restrict__ dlogits) {
+    __shared__ float acc[4][64 * Q];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    if (t >= T) return;
+    const void *row = static_cast<const char *>(logits) + t * ld * (BF16 ? 2 : 4);
+    float l[Q], p[Q], one_minus[Q], g[Q];
+    float m = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        l[q] = lane + 64 * q < r.E ? load_logit<BF16>(row, lane + 64 * q) : -INFINITY;
+        m = fmaxf(m, l[q]);
+    }
+    if (r.softmax) m = wave_max_f32(m, kWave);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        p[q] = r.softmax ? softmax_term(l[q], m) : sigmoid_f32(l[q]);
+        one_minus[q] = r.softmax ? 1.f : sigmoid_f32(-l[q]);
+        total += p[q];
+        acc[wave][lane + 64 * q] = 0.f;
+    }
+    total = wave_sum_f32(total);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        p[q] = total == 0.f ? 0.f : p[q] / total;  // shares of the whole row
+        g[q] = 0.f;
+    }
+    wave_sync();
+    if (dw) {
+        const int e = lane < r.k ? idx[t * r.k + lane] : -1;
+        const bool on = e >= 0 && e < r.E;
+        const float le = on ? load_logit<BF16>(row, e) : -INFINITY;
+        const float c = on ? r.scale * dw[t * r.k + lane] : 0.f;
+        float d = 0.f;
+        if (r.renorm) {
+            const float mc = wave_max_f32(le, kWave);
+            const float s = !on ? 0.f : r.softmax ? softmax_term(le, mc) : sigmoid_f32(le);
+            const float S = wave_sum_f32(s);
+            const float share = S == 0.f ? 0.f : s / S;
+            d = share * (c - wave_sum_f32(c * share)) * (r.softmax ? 1.f : sigmoid_f32(-le));
+        } else if (r.softmax) {
+            const float pe = on && total != 0.f ? softmax_term(le, m) / total : 0.f;
+            d = c * pe;
+            const float mean = wave_sum_f32(d);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) g[q] -= p[q] * mean;
+        } else {
+            d = on ? c * sigmoid_f32(le) * sigmoid_f32(-le) : 0.f;
+        }
+        if (on) acc[wave][e] = d;
+    }
+    wave_sync();
+    if (b.seq) {
+        const int n = b.n_seq, q0 = sequence_of(b.seq, n, (int)t);
+        const int start = q0 < n ? b.seq[q0] : T, end = q0 < n ? b.seq[q0 + 1] : T;
+        if (t >= start && t < end) {
+            const float c = b.alpha * b.dloss[q0] / (float)(end - start);
+            float f[Q], dot = 0.f;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                f[q] = lane + 64 * q < r.E ? c * b.load[(int64_t)q0 * r.E + lane + 64 * q] : 0.f;
+                dot += f[q] * p[q];
+            }
+            dot = wave_sum_f32(dot);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) g[q] += p[q] * (f[q] - dot) * one_minus[q];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        if (lane + 64 * q < r.E) dlogits[t * r.E + lane + 64 * q] = g[q] + acc[wave][lane + 64 * q];
+}
+
+// Partial sums of the balance loss: a workgroup takes kBalanceTokens tokens and
+// walks the sequences that lie in them; each (workgroup, sequence) pair owns
+// slot workgroup + sequence (ascending in both, so no two share one), where it
+// leaves the sum of the tokens' shares and the count of choices per expert.
+template <int Q, bool BF16>
+__global__ __launch_bounds__(256) void k_balance_part(SelectRule r, int T, const void *__restrict__ logits, int64_t ld,
+                                                      const int32_t *__restrict__ idx, const int32_t *__restrict__ seq,
+                                                      int n_seq, float *__restrict__ part, int32_t *__restrict__ count) {
+    __shared__ float share[4][64 * Q];
+    __shared__ int32_t hist[64 * Q];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int t1 = min((int)min((int64_t)(blockIdx.x + 1) * kBalanceTokens, (int64_t)T), T);
+    int t = max((int)((int64_t)blockIdx.x * kBalanceTokens), seq[0]);
+    while (t < t1) {
+        const int s = sequence_of(seq, n_seq, t);
+        if (s >= n_seq) break;
+        const int end = max(t + 1, min(t1, seq[s + 1]));
+        for (int e = tid; e < 64 * Q; e += 256) hist[e] = 0;
+        float sum[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) sum[q] = 0.f;
+        for (int u = t + wave; u < end; u += 4) {
+            const void *row = static_cast<const char *>(logits) + (int64_t)u * ld * (BF16 ? 2 : 4);
+            float p[Q], m = -INFINITY, total = 0.f;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                p[q] = lane + 64 * q < r.E ? load_logit<BF16>(row, lane + 64 * q) : -INFINITY;
+                m = fmaxf(m, p[q]);
+            }
+            if (r.softmax) m = wave_max_f32(m, kWave);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                p[q] = r.softmax ? softmax_term(p[q], m) : sigmoid_f32(p[q]);
+                total += p[q];
+            }
+            total = wave_sum_f32(total);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) sum[q] += total == 0.f ? 0.f : p[q] / total;
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) share[wave][lane + 64 * q] = sum[q];
+        __syncthreads();
+        for (int i = t * r.k + tid; i < end * r.k; i += 256) {
+            const int e = idx[i];
+            if (e >= 0 && e < r.E) atomicAdd(&hist[e], 1);
+        }
+        __syncthreads();
+        const int64_t slot = (int64_t)blockIdx.x + s;
+        for (int e = tid; e < r.E; e += 256) {
+            part[slot * r.E + e] = share[0][e] + share[1][e] + share[2][e] + share[3][e];
+            count[slot * r.E + e] = hist[e];
+        }
+        __syncthreads();
+        t = end;
+    }
+}
+
+// One workgroup per sequence: its slots added in order, load_e = E count_e /
+// (k n), loss = alpha sum_e load_e mean_e.  A sequence without tokens has no
+// loss and no load.
+__global__ __launch_bounds__(256) void k_balance_sum(int E, int k, int T, const int32_t *__restrict__ seq, float alpha,
+                                                     const float *__restrict__ part, const int32_t *__restrict__ count,
+                                                     float *__restrict__ loss, float *__restrict__ load) {
+    __shared__ double wsum[4];
+    const int s = blockIdx.x, tid = threadIdx.x;
+    const int a = min(max(seq[s], 0), T), b = min(max(seq[s + 1], 0), T), n = b - a;
+    double mine = 0.0;
+    for (int e = tid; e < E; e += 256) {
+        double sum = 0.0;
+        int64_t c = 0;
+        if (n > 0)
+            for (int64_t i = a / kBalanceTokens + s; i <= (int64_t)(b - 1) / kBalanceTokens + s; ++i) {
+                sum += part[i * E + e];
+                c += count[i * E + e];
+            }
+        const double f = n > 0 ? (double)E * (double)c / ((double)k * n) : 0.0;
+        load[(int64_t)s * E + e] = (float)f;
+        if (n > 0) mine += f * sum / n;
+    }
+    mine = wave_sum_f64(mine);
+    if ((tid & 63) == 0) wsum[tid >> 6] = mine;
+    __syncthreads();
+    if (tid == 0) loss[s] = (float)((double)alpha * (wsum[0] + wsum[1] + wsum[2] + wsum[3]));
+}
+
+int balance_blocks(int T) { return (T + kBalanceTokens - 1) / kBalanceTokens; }
+
+}  // namespace
+
+// Experts per lane: the next power of two of E / 64.
+#define MOE_BY_WIDTH(LAUNCH)                       \
+    do {                                           \
+        if (a.rule.E <= 64) LAUNCH(1);             \
+        else if (a.rule.E <= 128) LAUNCH(2);       \
+        else if (a.rule.E <= 256) LAUNCH(4);       \
+        else if (a.rule.E <= 512) LAUNCH(8);       \
+        else LAUNCH(16);                           \
+    } while (0)
+
+hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)(((int64_t)a.T + 3) / 4)), block(256);
+#define GO(Q)                                                                                                        \
+    do {                                                                                                             \
+        if (a.bf16) hipLaunchKernelGGL((k_select<Q, true>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld, a.bias,   \
+                                       a.idx, a.weights);                                                            \
+        else hipLaunchKernelGGL((k_select<Q, false>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld, a.bias, a.idx, \
+                                a.weights);                                                                          \
+    } while (0)
+    MOE_BY_WIDTH(GO);
+#undef GO
+    return hipGetLastError();
+}
+
+hipError_t launch_select_backward(const SelectBackwardArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)(((int64_t)a.T + 3) / 4)), block(256);
+#define GO(Q)                                                                                                     \
+    do {                                                                                                          \
+        if (a.bf16) hipLaunchKernelGGL((k_select_backward<Q, true>), grid, block, 0, s, a.rule, a.T, a.logits,     \
+                                       a.ld, a.idx, a.dweights, a.balance, a.dlogits);                            \
+        else hipLaunchKernelGGL((k_select_backward<Q, false>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld,    \
+                                a.idx, a.dweights, a.balance, a.dlogits);                                         \
+    } while (0)
+    MOE_BY_WIDTH(GO);
+#undef GO
+    return hipGetLastError();
+}
+
+size_t balance_ws_bytes(int T, int E, int n_seq) {
+    return ((size_t)balance_blocks(T) + n_seq) * E * (sizeof(float) + sizeof(int32_t));
+}
+
+hipError_t launch_balance_loss(const BalanceArgs &a, void *ws, hipStream_t s) {
+    const size_t slots = (size_t)balance_blocks(a.T) + a.n_seq;
+    float *part = static_cast<float *>(ws);
+    int32_t *count = reinterpret_cast<int32_t *>(part + slots * a.rule.E);
+    const dim3 grid(balance_blocks(a.T)), block(256);
+#define GO(Q)                                                                                                       \
+    do {                                                                                                            \
+        if (a.bf16) hipLaunchKernelGGL((k_balance_part<Q, true>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld,   \
+                                       a.idx, a.seq, a.n_seq, part, count);                                         \
+        else hipLaunchKernelGGL((k_balance_part<Q, false>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld, a.idx,  \
+                                a.seq, a.n_seq, part, count);                                                       \
+    } while (0)
+    MOE_BY_WIDTH(GO);
+#undef GO
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_balance_sum, dim3(a.n_seq), block, 0, s, a.rule.E, a.rule.k, a.T, a.seq, a.alpha, part, count,
+                       a.loss, a.load);
+    return hipGetLastError();
+}
+#undef MOE_BY_WIDTH
+
+}  // namespace moe
