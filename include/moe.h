@@ -344,7 +344,10 @@ moe_status_t moe_router_logits(const moe_desc_t *desc, const void *x, const floa
  *   dx        [T, d] fp32 out
  *   dw_router [E, d] fp32 out (written, not accumulated)
  *   workspace >= moe_workspace_bytes(desc, MOE_WS_ROUTER_GRAD) bytes
- * Deterministic.
+ * x, dlogits, dw_router and the workspace are 16-byte aligned.  fp32's accuracy,
+ * relative to the largest of a row of dlogits and of a column of w_router for dx,
+ * to the terms themselves for dw_router; a sum that an infinity or a NaN enters is
+ * NaN.  Deterministic.
  */
 moe_status_t moe_router_logits_backward(const moe_desc_t *desc, const void *x, const float *w_router,
                                         const float *dlogits, const float *dx_in, float *dx, float *dw_router,

@@ -495,6 +495,7 @@ moe_status_t moe_router_logits_backward(const moe_desc_t *d, const void *x, cons
     moe_status_t st = check_desc(d);
     if (st != MOE_OK) return st;
     if (!x || !w_router || !dlogits || !dx || !dw_router) return MOE_EINVAL;
+    if (!aligned16(x) || !aligned16(dlogits) || !aligned16(dw_router) || !aligned16(workspace)) return MOE_EINVAL;
     const size_t need = router_grad_ws(d);
     if (need && (!workspace || ws_bytes < need)) return MOE_EWORKSPACE;
     const moe::RouterGradArgs a{d->T, d->d, d->act == MOE_BF16, x, w_router, dlogits, dx_in, dx, dw_router};

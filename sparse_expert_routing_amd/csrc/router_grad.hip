@@ -1,7 +1,17 @@
 // The router projection's gradient from that of its logits:
 //   dx[t, n] = dx_in[t, n] + sum_e dl[t, e] w[e, n],   dw[e, n] = sum_t dl[t, e] x[t, n]
-// in fp32.  64x64 tiles, 16 of the reduction per stage through LDS, 4x4 sums per
-// thread.
+// with fp32's accuracy, on the 16-bit matrix cores (16x the fp32 ones' rate).
+//
+// Each fp32 operand becomes a few 16-bit terms whose products are exact in fp32:
+//   - dx, K = 256: a row of dl and a column of w are each scaled by a power of
+//     two so that their largest magnitude lies in [2^14, 2^15), then v = hi + mid
+//     in fp16 (hi = rne(v), mid = rne(v - hi): 22 bits, down to 2^-39 of the
+//     row's largest).  hi hi + hi mid + mid hi leaves out mid mid, 2^-22 of a
+//     product; the sum is scaled back by the two exponents together (ldexp).
+//   - dw, K = T: x is bf16 as it is; dl = hi + mid + lo in bf16, each the top 8
+//     bits of what is left, 24 bits and exact.  An fp32 x is split the same way,
+//     and the six products of at least 2^-16 of the whole are summed.
+// An infinity or NaN in dl, w or an fp32 x makes the sums it enters NaN.
 #include "device.h"
 #include "kernels.h"
 
@@ -10,60 +20,425 @@ namespace moe {
 namespace {
 
 constexpr int kE = 256;
-constexpr int kT = 64, kK = 16;
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 *lds_i16x4_t;
+typedef __attribute__((address_space(3))) void lds_void;
 
-// C[m, n] = C_in[m, n] + sum_k A(m, k) B(k, n); A(m, k) = a[m*256 + k] (M = T, K =
-// 256) or, transposed, a[k*256 + m] (M = 256, K = T); B(k, n) = b[k*N + n].
-template <bool TRANS, bool B16>
-__global__ __launch_bounds__(256) void k_tile_gemm(int M, int N, int K, const float *__restrict__ a,
-                                                   const void *__restrict__ b, const float *__restrict__ cin,
-                                                   float *__restrict__ c) {
-    __shared__ float sa[kK][kT + 4], sb[kK][kT + 4];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int64_t m0 = (int64_t)blockIdx.y * kT;
-    const int n0 = blockIdx.x * kT;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += kK) {
-        __syncthreads();
-        for (int i = tid; i < kK * kT; i += 256) {
-            const int k = TRANS ? i / kT : i % kK, m = TRANS ? i % kT : i / kK;
-            const bool in = m0 + m < M && k0 + k < K;
-            sa[k][m] = !in ? 0.f : TRANS ? a[(int64_t)(k0 + k) * kE + m0 + m] : a[(m0 + m) * kE + k0 + k];
-            const int kb = i / kT, n = i % kT;
-            const int64_t at = (int64_t)(k0 + kb) * N + n0 + n;
-            sb[kb][n] = k0 + kb >= K ? 0.f
-                        : B16        ? bf16_to_f32(static_cast<const uint16_t *>(b)[at])
-                                     : static_cast<const float *>(b)[at];
+__device__ __forceinline__ void dma16(const void *src, void *lds) {
+    __builtin_amdgcn_global_load_lds(src, (lds_void *)lds, 16, 0, 0);
+}
+// This wave's loads and LDS reads are done, and every wave's.
+__device__ __forceinline__ void all_landed() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt((7 << 4));  // vmcnt(0), lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// The exponent e of the scale 2^e that brings a largest magnitude (its bits)
+// into [2^14, 2^15); 0 for zero, and no more than 2^126, which fp32's
+// subnormals do not fill.
+__device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
+    if (amax_bits == 0) return 0;
+    return min(14 - ((int)(amax_bits >> 23) - 127), 126);
+}
+
+__device__ __forceinline__ uint32_t f16_bits(_Float16 v) { return (uint32_t)__builtin_bit_cast(uint16_t, v); }
+
+// v = hi + mid in fp16 (bits).
+__device__ __forceinline__ void split_f16(float v, uint32_t &hi, uint32_t &mid) {
+    const _Float16 h = (_Float16)v;
+    hi = f16_bits(h);
+    mid = f16_bits((_Float16)(v - (float)h));
+}
+
+// v = t[0] + t[1] + t[2] in bf16 (bits), each the top of what is left: exact.
+__device__ __forceinline__ void split_bf16(float v, uint32_t (&t)[3]) {
+    t[0] = __float_as_uint(v) >> 16;
+    v -= bf16_to_f32(t[0]);
+    t[1] = __float_as_uint(v) >> 16;
+    v -= bf16_to_f32(t[1]);
+    t[2] = __float_as_uint(v) >> 16;
+}
+
+struct RgWs {
+    uint16_t *dlh;   // [2][T][256] fp16 terms of the scaled rows of dl
+    int32_t *er;     // [T] their exponents
+    uint16_t *wh;    // [2][d][256] fp16 terms of the scaled columns of w
+    int32_t *ec;     // [d]
+    uint16_t *dlt;   // [3][256][Tp] bf16 terms of dl, transposed, zeros behind T
+    uint16_t *xs;    // [3][T][d] bf16 terms of an fp32 x
+    float *part;     // [S][256][d] partial sums of dw
+    int Tp, S;
+    size_t bytes;
+};
+
+constexpr int kStageK = 32;  // K per stage of the dw product
+
+// Splits of dw's K = T range: about one workgroup per CU, four stages at least
+// each.  Neighbouring workgroups take different splits, so with a multiple of 8
+// each XCD works on its own tokens and keeps their dl terms in its L2.
+int dw_splits(int T, int d) {
+    const int tiles = (d + 255) / 256, stages = (T + kStageK - 1) / kStageK;
+    int S = 256 / tiles;
+    if (S > 8) S = S / 8 * 8;
+    const int most = (stages + 3) / 4;
+    return S < 1 ? 1 : S > most ? most : S;
+}
+
+RgWs carve(char *base, int T, int d, bool x_bf16) {
+    RgWs w{};
+    size_t o = 0;
+    auto take = [&](size_t n) -> char * {
+        char *p = base ? base + o : nullptr;
+        o += (n + 255) / 256 * 256;
+        return p;
+    };
+    w.Tp = (T + kStageK - 1) / kStageK * kStageK;
+    w.S = dw_splits(T, d);
+    w.dlh = reinterpret_cast<uint16_t *>(take((size_t)2 * T * kE * 2));
+    w.er = reinterpret_cast<int32_t *>(take((size_t)w.Tp * 4));
+    w.wh = reinterpret_cast<uint16_t *>(take((size_t)2 * d * kE * 2));
+    w.ec = reinterpret_cast<int32_t *>(take((size_t)d * 4));
+    w.dlt = reinterpret_cast<uint16_t *>(take((size_t)3 * kE * w.Tp * 2));
+    w.xs = x_bf16 ? nullptr : reinterpret_cast<uint16_t *>(take((size_t)3 * T * d * 2));
+    w.part = w.S == 1 ? nullptr : reinterpret_cast<float *>(take((size_t)w.S * kE * d * 4));
+    w.bytes = o;
+    return w;
+}
+
+// The operands' terms in one launch.  Workgroups [0, nw): 64 columns of w each;
+// [nw, nw + nt): 32 rows of dl each; the rest, for an fp32 x: 1024 of its values.
+__global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, const float *__restrict__ w,
+                                                  const float *__restrict__ dl, const float *__restrict__ x, RgWs ws) {
+    __shared__ float tile[32][kE];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if ((int)blockIdx.x < nw) {
+        // thread: column n, experts 64 wave .. +63
+        const int n = blockIdx.x * 64 + lane;
+        float v[64];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+            v[i] = w[(int64_t)(wave * 64 + i) * d + n];
+            m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
         }
+        uint32_t *most = reinterpret_cast<uint32_t *>(&tile[0][0]);
+        most[tid] = m;
         __syncthreads();
+        m = max(max(most[lane], most[64 + lane]), max(most[128 + lane], most[192 + lane]));
+        const int e = scale_exp(m);
+        if (wave == 0) ws.ec[n] = -e;
 #pragma unroll
-        for (int k = 0; k < kK; ++k)
+        for (int c = 0; c < 8; ++c) {
+            i32x4 hi, mid;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty * 4 + i] * sb[k][tx * 4 + j];
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h0, m0, h1, m1;
+                split_f16(ldexpf(v[8 * c + 2 * i], e), h0, m0);
+                split_f16(ldexpf(v[8 * c + 2 * i + 1], e), h1, m1);
+                hi[i] = (int)(h0 | (h1 << 16));
+                mid[i] = (int)(m0 | (m1 << 16));
+            }
+            uint16_t *o = ws.wh + (int64_t)n * kE + wave * 64 + 8 * c;
+            *reinterpret_cast<i32x4 *>(o) = hi;
+            *reinterpret_cast<i32x4 *>(o + (int64_t)d * kE) = mid;
+        }
+        return;
     }
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty * 4 + i;
-        if (m >= M) continue;
-        for (int j = 0; j < 4; ++j) {
-            const int64_t at = m * N + n0 + tx * 4 + j;
-            c[at] = acc[i][j] + (cin ? cin[at] : 0.f);
+    if ((int)blockIdx.x >= nw + nt) {
+        const int64_t at = ((int64_t)(blockIdx.x - nw - nt) * 256 + tid) * 4, n = (int64_t)T * d;
+        if (at >= n) return;  // n is a multiple of 4
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(x + at);
+        uint32_t t[4][3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_bf16(v[i], t[i]);
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            *reinterpret_cast<uint2 *>(ws.xs + j * n + at) = uint2{t[0][j] | (t[1][j] << 16), t[2][j] | (t[3][j] << 16)};
+        return;
+    }
+    const int t0 = (blockIdx.x - nw) * 32;
+    for (int r = wave; r < 32; r += 4) {  // a wave per row: 4 experts per lane
+        const int t = t0 + r;
+        f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (t < T) v = *reinterpret_cast<const f32x4 *>(dl + (int64_t)t * kE + 4 * lane);
+        *reinterpret_cast<f32x4 *>(&tile[r][4 * lane]) = v;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        for (int s = 32; s >= 1; s >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, s, kWave));
+        const int e = scale_exp(m);
+        if (lane == 0) ws.er[t] = -e;
+        if (t >= T) continue;
+        uint32_t h[4], q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_f16(ldexpf(v[i], e), h[i], q[i]);
+        uint16_t *o = ws.dlh + (int64_t)t * kE + 4 * lane;
+        *reinterpret_cast<uint2 *>(o) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+        *reinterpret_cast<uint2 *>(o + (int64_t)T * kE) = uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
+    }
+    __syncthreads();
+    // thread: expert tid, its 32 tokens in a row
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        i32x4 o[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a[3], b[3];
+            split_bf16(tile[8 * c + 2 * i][tid], a);
+            split_bf16(tile[8 * c + 2 * i + 1][tid], b);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) o[j][i] = (int)(a[j] | (b[j] << 16));
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            *reinterpret_cast<i32x4 *>(ws.dlt + ((int64_t)j * kE + tid) * ws.Tp + t0 + 8 * c) = o[j];
+    }
+}
+
+// ------------------------------------------------------------------- dx
+
+constexpr int kDxN = 128;  // columns per workgroup
+
+// Position of 16-byte piece c of row r in an LDS tile of 512-byte rows: rows
+// that are read together lie in different banks.
+__device__ __forceinline__ int piece512(int r, int c) { return r * kE + ((c ^ (r & 7) ^ ((r >> 3) & 1)) * 8); }
+
+// A workgroup keeps its 128 columns' terms of w in LDS (128 KB) and its 8 waves
+// walk 32-token chunks: their dl terms come straight from memory (each wave
+// has its own rows, so LDS would not save a read), there is no barrier in the
+// loop.  32x32x16 tiles, 4 per wave; lane: column n, so a store is 128 bytes of a row.
+__global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, const float *__restrict__ dx_in,
+                                                  float *__restrict__ dx) {
+    __shared__ __attribute__((aligned(1024))) uint16_t sw[2 * kDxN * kE];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n0 = blockIdx.y * kDxN;
+    // 256 rows (term, n) of 512 bytes, two per load instruction
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * (wave * 16 + i) + g, n = min(n0 + (r & (kDxN - 1)), d - 1);
+        const int c = (lane & 31) ^ (r & 7) ^ ((r >> 3) & 1);
+        dma16(ws.wh + ((int64_t)(r / kDxN) * d + n) * kE + 8 * c, sw + 2 * (wave * 16 + i) * kE);
+    }
+    const int chunks = (T + 31) / 32, S = gridDim.x, z = blockIdx.x;
+    const int c0 = (int)((int64_t)chunks * z / S), c1 = (int)((int64_t)chunks * (z + 1) / S);
+    int ec[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ec[j] = ws.ec[min(n0 + 32 * j + (lane & 31), d - 1)];
+    all_landed();
+    // LDS: row 32 j + lane % 32 of term m at + 16 KB j + 64 KB m, piece 2 ks + g by one xor
+    const uint32_t row_off = (uint32_t)piece512(lane & 31, g);
+    f16x8 a[2][2][4];  // quarter of K (even, odd), term, step
+    auto load = [&](int ch, int q, f16x8 (&v)[2][4]) {
+        const uint16_t *p = ws.dlh + (int64_t)min(ch * 32 + (lane & 31), T - 1) * kE + 8 * g + 64 * q;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            v[0][s] = *reinterpret_cast<const f16x8 *>(p + 16 * s);
+            v[1][s] = *reinterpret_cast<const f16x8 *>(p + (int64_t)T * kE + 16 * s);
+        }
+    };
+    f32x16 acc[4];
+    auto quarter = [&](int q, const f16x8 (&v)[2][4]) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint16_t *h = sw + (row_off ^ (uint32_t)(16 * (4 * q + s))), *m = h + kDxN * kE;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f16x8 bh = *reinterpret_cast<const f16x8 *>(h + 32 * j * kE);
+                const f16x8 bm = *reinterpret_cast<const f16x8 *>(m + 32 * j * kE);
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[1][s], bh, acc[j], 0, 0, 0);
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0][s], bm, acc[j], 0, 0, 0);
+                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0][s], bh, acc[j], 0, 0, 0);
+            }
+        }
+    };
+    if (c0 + wave < c1) load(c0 + wave, 0, a[0]);
+    for (int ch = c0 + wave; ch < c1; ch += 8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = f32x16{};
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
+            load(ch, q + 1, a[1]);
+            quarter(q, a[0]);
+            if (q == 0) load(ch, 2, a[0]);
+            else load(min(ch + 8, c1 - 1), 0, a[0]);  // the next chunk's
+            quarter(q + 1, a[1]);
+        }
+        // lane: column n0 + 32 j + lane % 32, tokens t0 + 8 q + 4 g + r
+        const int t0 = ch * 32 + 4 * g, n = n0 + (lane & 31);
+        const bool whole = ch * 32 + 32 <= T && n0 + kDxN <= d;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const i32x4 er = *reinterpret_cast<const i32x4 *>(ws.er + t0 + 8 * q);
+            const int64_t at = (int64_t)(t0 + 8 * q) * d + n;
+            float in[4][4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    in[r][j] = dx_in && (whole || (t0 + 8 * q + r < T && n + 32 * j < d)) ? dx_in[at + (int64_t)r * d + 32 * j]
+                                                                                         : 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float v = ldexpf(acc[j][4 * q + r], er[r] + ec[j]) + in[r][j];
+                    if (whole || (t0 + 8 * q + r < T && n + 32 * j < d)) dx[at + (int64_t)r * d + 32 * j] = v;
+                }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
 
+// ------------------------------------------------------------------- dw
+
+constexpr int kDwN = 256;  // columns per workgroup
+
+// Position of 16-byte piece c of row r in the A tile's 64-byte rows.
+__device__ __forceinline__ int piece64(int r, int c) { return r * kStageK + ((c ^ ((r >> 1) & 3)) * 8); }
+
+// 256 experts x 256 columns per workgroup, 8 waves of 64 x 128, two stages of
+// K = 32 in LDS: three terms of dl^T (48 KB) and NX terms of x (16 KB each),
+// both by direct loads.  x lies K-major and is read with transposing LDS reads:
+// within each 16 lanes, lane 4a + c receives element c of the 8 bytes that lanes
+// a, a+4, a+8, a+12 point at; its 16-byte piece c of row k sits at c ^ 4 (k % 4).
+template <int NX>
+__global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, const uint16_t *__restrict__ x,
+                                                  float *__restrict__ out) {
+    constexpr int kA = 3 * kE * kStageK, kX = kStageK * kDwN;  // elements per stage
+    constexpr int kNStage = NX == 1 ? 2 : 1;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[kNStage * (kA + NX * kX)];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int S = ws.S, z = blockIdx.x % S, n0 = (blockIdx.x / S) * kDwN;
+    const int stages = ws.Tp / kStageK;
+    const int s0 = (int)((int64_t)stages * z / S), s1 = (int)((int64_t)stages * (z + 1) / S);
+    out += (int64_t)z * kE * d;
+
+    auto issue = [&](int st, uint16_t *to) {
+        const int k0 = st * kStageK;
+        // A: 48 instructions of 16 rows; 6 per wave
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            const int blk = wave * 6 + i, r = 16 * blk + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
+            dma16(ws.dlt + (int64_t)r * ws.Tp + k0 + 8 * c, to + blk * 16 * kStageK);
+        }
+        // x: NX * 16 instructions of 2 rows; 2 NX per wave
+#pragma unroll
+        for (int i = 0; i < 2 * NX; ++i) {
+            const int blk = wave * 2 * NX + i, r = 2 * blk + g, k = r & (kStageK - 1);
+            const int t = min(k0 + k, T - 1), n = min(n0 + 8 * ((lane & 31) ^ (4 * (k & 3))), d - 8);
+            dma16(x + ((int64_t)(r / kStageK) * T + t) * d + n, to + kA + 2 * blk * kDwN);
+        }
+    };
+    f32x16 acc[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    auto step = [&](const uint16_t *st) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 a[3][2];
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    a[m][i] = *reinterpret_cast<const bf16x8 *>(
+                        st + piece64(m * kE + wm * 64 + 32 * i + (lane & 31), 2 * ks + g));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int u = 0; u < NX; ++u) {
+                    const int h = lane >> 4, b = lane & 15;
+                    const int k = 16 * ks + 8 * (h >> 1) + (b >> 2);
+                    const int col = wn * 128 + 32 * j + 16 * (h & 1) + 4 * (b & 3);
+                    const uint16_t *p = st + kA + u * kX + k * kDwN + ((((col >> 3) ^ (4 * (k & 3))) << 3) | (col & 7));
+                    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)p);
+                    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(p + 4 * kDwN));
+                    const bf16x8 xb =
+                        __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                    for (int m = 2 - u; m >= 0; --m)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m][i], xb, acc[i][j], 0, 0, 0);
+                }
+        }
+    };
+    if (kNStage == 2) {
+        constexpr int kBuf = kA + NX * kX;
+        if (s0 < s1) issue(s0, smem);
+        for (int st = s0; st < s1; ++st) {
+            all_landed();  // stage st is there, stage st - 1 no longer read
+            if (st + 1 < s1) issue(st + 1, smem + ((st + 1 - s0) & 1) * kBuf);
+            step(smem + ((st - s0) & 1) * kBuf);
+        }
+    } else {
+        for (int st = s0; st < s1; ++st) {
+            issue(st, smem);
+            all_landed();
+            step(smem);
+            all_landed();
+        }
+    }
+    // lane: column n0 + 128 wn + 32 j + lane % 32, experts 64 wm + 32 i + 8 q + 4 g + r
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + wn * 128 + 32 * j + (lane & 31);
+            if (n >= d) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    out[(int64_t)(wm * 64 + 32 * i + 8 * q + 4 * g + r) * d + n] = acc[i][j][4 * q + r];
+        }
+}
+
+// dw = the S partial sums added in order, 4 values per thread.
+__global__ __launch_bounds__(256) void k_rg_sum(int64_t n4, int S, const f32x4 *__restrict__ part,
+                                                f32x4 *__restrict__ dw) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    f32x4 v = part[i];
+#pragma unroll 4
+    for (int z = 1; z < S; ++z) v += part[(int64_t)z * n4 + i];
+    dw[i] = v;
+}
+
 }  // namespace
 
-size_t router_grad_ws_bytes(int, int, bool) { return 0; }
+size_t router_grad_ws_bytes(int T, int d, bool x_bf16) { return carve(nullptr, T, d, x_bf16).bytes; }
 
-hipError_t launch_router_grad(const RouterGradArgs &a, void *, hipStream_t s) {
-    const dim3 block(256), gx(a.d / kT, (a.T + kT - 1) / kT), gw(a.d / kT, kE / kT);
-    hipLaunchKernelGGL((k_tile_gemm<false, false>), gx, block, 0, s, a.T, a.d, kE, a.dlogits, a.w, a.dx_in, a.dx);
+hipError_t launch_router_grad(const RouterGradArgs &a, void *workspace, hipStream_t s) {
+    const int T = a.T, d = a.d;
+    const RgWs ws = carve(static_cast<char *>(workspace), T, d, a.x_bf16);
+    const int nw = d / 64, nt = ws.Tp / 32;
+    const int64_t nx = a.x_bf16 ? 0 : ((int64_t)T * d / 4 + 255) / 256;
+    if (nw + nt + nx > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_rg_split, dim3((unsigned)(nw + nt + nx)), dim3(256), 0, s, T, d, nw, nt, a.w, a.dlogits,
+                       static_cast<const float *>(a.x_bf16 ? nullptr : a.x), ws);
+    // dx: about one workgroup per CU, at least one round of 8 chunks each
+    const int ntile = (d + kDxN - 1) / kDxN, rounds = (T + 255) / 256;
+    const int S = 256 / ntile < 1 ? 1 : 256 / ntile > rounds ? rounds : 256 / ntile;
+    hipLaunchKernelGGL(k_rg_dx, dim3(S, ntile), dim3(512), 0, s, T, d, ws, a.dx_in, a.dx);
+    float *out = ws.S == 1 ? a.dw : ws.part;
+    const dim3 grid((unsigned)(ws.S * ((d + kDwN - 1) / kDwN)));
     if (a.x_bf16)
-        hipLaunchKernelGGL((k_tile_gemm<true, true>), gw, block, 0, s, kE, a.d, a.T, a.dlogits, a.x, nullptr, a.dw);
+        hipLaunchKernelGGL(k_rg_dw<1>, grid, dim3(512), 0, s, T, d, ws, static_cast<const uint16_t *>(a.x), out);
     else
-        hipLaunchKernelGGL((k_tile_gemm<true, false>), gw, block, 0, s, kE, a.d, a.T, a.dlogits, a.x, nullptr, a.dw);
+        hipLaunchKernelGGL(k_rg_dw<3>, grid, dim3(512), 0, s, T, d, ws, ws.xs, out);
+    if (ws.S > 1) {
+        const int64_t n4 = (int64_t)kE * d / 4;
+        hipLaunchKernelGGL(k_rg_sum, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, n4, ws.S,
+                           reinterpret_cast<const f32x4 *>(ws.part), reinterpret_cast<f32x4 *>(a.dw));
+    }
     return hipGetLastError();
 }
 

@@ -144,6 +144,10 @@ def test_router_logits_refusals():
     for i in (0, 1, 2, 4, 5):
         a = [None if i == j else P for j in range(6)]
         assert L.moe_router_logits_backward(ctypes.byref(ds), *a, P, need, None) == EINVAL
+    assert need > 0
+    for i in (0, 2, 5):  # not 16-byte aligned
+        a = [P + 4 if i == j else P for j in range(6)]
+        assert L.moe_router_logits_backward(ctypes.byref(ds), *a, P, need, None) == EINVAL
     if need:
         assert L.moe_router_logits_backward(ctypes.byref(ds), P, P, P, None, P, P, P, need - 1, None) == EWORKSPACE
     assert L.moe_router_logits_backward(ctypes.byref(good_desc(E=64)), P, P, P, None, P, P, P, need, None) == ENOTSUP
