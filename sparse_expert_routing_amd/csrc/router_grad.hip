@@ -62,28 +62,31 @@ __device__ __forceinline__ void split_bf16(float v, uint32_t (&t)[3]) {
     t[2] = __float_as_uint(v) >> 16;
 }
 
+// Position of 16-byte piece c of row r in the dw product's A tiles, rows of 32
+// bytes: eight rows that are read together lie in different banks.
+constexpr int kStageK = 16;  // K per stage of the dw product
+__device__ __forceinline__ int piece32(int r, int c) { return r * kStageK + ((c ^ ((r >> 2) & 1)) * 8); }
+
 struct RgWs {
     uint16_t *dlh;   // [2][T][256] fp16 terms of the scaled rows of dl
     int32_t *er;     // [T] their exponents
     uint16_t *wh;    // [2][d][256] fp16 terms of the scaled columns of w
     int32_t *ec;     // [d]
-    uint16_t *dlt;   // [3][256][Tp] bf16 terms of dl, transposed, zeros behind T
+    uint16_t *dlt;   // [Tp/16][3][256][16] bf16 terms of dl, transposed by stages of 16 tokens, zeros behind T
     uint16_t *xs;    // [3][T][d] bf16 terms of an fp32 x
     float *part;     // [S][256][d] partial sums of dw
     int Tp, S;
     size_t bytes;
 };
 
-constexpr int kStageK = 32;  // K per stage of the dw product
-
-// Splits of dw's K = T range: about one workgroup per CU, four stages at least
+// Splits of dw's K = T range: about one workgroup per CU, eight stages at least
 // each.  Neighbouring workgroups take different splits, so with a multiple of 8
 // each XCD works on its own tokens and keeps their dl terms in its L2.
 int dw_splits(int T, int d) {
     const int tiles = (d + 255) / 256, stages = (T + kStageK - 1) / kStageK;
     int S = 256 / tiles;
     if (S > 8) S = S / 8 * 8;
-    const int most = (stages + 3) / 4;
+    const int most = (stages + 7) / 8;
     return S < 1 ? 1 : S > most ? most : S;
 }
 
@@ -95,7 +98,7 @@ RgWs carve(char *base, int T, int d, bool x_bf16) {
         o += (n + 255) / 256 * 256;
         return p;
     };
-    w.Tp = (T + kStageK - 1) / kStageK * kStageK;
+    w.Tp = (T + 31) / 32 * 32;
     w.S = dw_splits(T, d);
     w.dlh = reinterpret_cast<uint16_t *>(take((size_t)2 * T * kE * 2));
     w.er = reinterpret_cast<int32_t *>(take((size_t)w.Tp * 4));
@@ -194,7 +197,8 @@ __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, 
         }
 #pragma unroll
         for (int j = 0; j < 3; ++j)
-            *reinterpret_cast<i32x4 *>(ws.dlt + ((int64_t)j * kE + tid) * ws.Tp + t0 + 8 * c) = o[j];
+            *reinterpret_cast<i32x4 *>(ws.dlt + ((int64_t)(t0 / kStageK + c / 2) * 3 + j) * kE * kStageK +
+                                       piece32(tid, c & 1)) = o[j];
     }
 }
 
@@ -210,8 +214,8 @@ __device__ __forceinline__ int piece512(int r, int c) { return r * kE + ((c ^ (r
 // walk 32-token chunks: their dl terms come straight from memory (each wave
 // has its own rows, so LDS would not save a read), there is no barrier in the
 // loop.  32x32x16 tiles, 4 per wave; lane: column n, so a store is 128 bytes of a row.
-__global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, const float *__restrict__ dx_in,
-                                                  float *__restrict__ dx) {
+__global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, const int32_t *__restrict__ er,
+                                                  const float *dx_in, float *dx) {
     __shared__ __attribute__((aligned(1024))) uint16_t sw[2 * kDxN * kE];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -255,41 +259,59 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
             }
         }
     };
-    if (c0 + wave < c1) load(c0 + wave, 0, a[0]);
+    // Stores count as loads in flight do, in order: two quarters of the next chunk are asked for
+    // ahead of a chunk's stores, so nothing waits for the stores but what comes a quarter later.
+    if (c0 + wave < c1) {
+        load(c0 + wave, 0, a[0]);
+        load(c0 + wave, 1, a[1]);
+    }
     for (int ch = c0 + wave; ch < c1; ch += 8) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[j] = f32x16{};
-#pragma unroll 1
-        for (int q = 0; q < 4; q += 2) {
-            load(ch, q + 1, a[1]);
-            quarter(q, a[0]);
-            if (q == 0) load(ch, 2, a[0]);
-            else load(min(ch + 8, c1 - 1), 0, a[0]);  // the next chunk's
-            quarter(q + 1, a[1]);
-        }
-        // lane: column n0 + 32 j + lane % 32, tokens t0 + 8 q + 4 g + r
+        quarter(0, a[0]);
+        __builtin_amdgcn_sched_barrier(0);
+        load(ch, 2, a[0]);
+        quarter(1, a[1]);
+        __builtin_amdgcn_sched_barrier(0);
+        load(ch, 3, a[1]);
+        // lane: column n0 + 32 j + lane % 32, tokens t0 + 8 q + 4 g + r; what is added to the
+        // sums is asked for here, half the products ahead of its use
         const int t0 = ch * 32 + 4 * g, n = n0 + (lane & 31);
         const bool whole = ch * 32 + 32 <= T && n0 + kDxN <= d;
+        const int64_t at0 = (int64_t)t0 * d + n;
+        f32x16 in[4];
+        if (dx_in == nullptr) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const i32x4 er = *reinterpret_cast<const i32x4 *>(ws.er + t0 + 8 * q);
-            const int64_t at = (int64_t)(t0 + 8 * q) * d + n;
-            float in[4][4];
+            for (int j = 0; j < 4; ++j) in[j] = f32x16{};
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    in[r][j] = dx_in && (whole || (t0 + 8 * q + r < T && n + 32 * j < d)) ? dx_in[at + (int64_t)r * d + 32 * j]
-                                                                                         : 0.f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int i = 0; i < 16; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float v = ldexpf(acc[j][4 * q + r], er[r] + ec[j]) + in[r][j];
-                    if (whole || (t0 + 8 * q + r < T && n + 32 * j < d)) dx[at + (int64_t)r * d + 32 * j] = v;
+                    const int row = 8 * (i >> 2) + (i & 3);
+                    in[j][i] = whole || (t0 + row < T && n + 32 * j < d) ? dx_in[at0 + (int64_t)row * d + 32 * j] : 0.f;
                 }
-            __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        quarter(2, a[0]);
+        __builtin_amdgcn_sched_barrier(0);
+        load(min(ch + 8, c1 - 1), 0, a[0]);
+        quarter(3, a[1]);
+        __builtin_amdgcn_sched_barrier(0);
+        load(min(ch + 8, c1 - 1), 1, a[1]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int lo = er[ch * 32 + 8 * q + r], hi = er[ch * 32 + 8 * q + 4 + r];  // wave-uniform
+                const int e = g ? hi : lo;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float v = ldexpf(acc[j][4 * q + r], e + ec[j]) + in[j][4 * q + r];
+                    if (whole || (t0 + 8 * q + r < T && n + 32 * j < d)) dx[at0 + (int64_t)(8 * q + r) * d + 32 * j] = v;
+                }
+            }
     }
 }
 
@@ -297,20 +319,28 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
 
 constexpr int kDwN = 256;  // columns per workgroup
 
-// Position of 16-byte piece c of row r in the A tile's 64-byte rows.
-__device__ __forceinline__ int piece64(int r, int c) { return r * kStageK + ((c ^ ((r >> 1) & 3)) * 8); }
+// A 16-byte load per lane into LDS, written as assembly: the compiler sees no
+// LDS write, so it does not wait for the loads in flight before the LDS reads
+// of a stage that has landed (it cannot tell the stages apart).  The loop's own
+// vmcnt waits and barriers order them.  The LDS address goes in through M0; the
+// s_nop covers the M0 write before the load.
+__device__ __forceinline__ void dma16_unseen(const void *src, const uint16_t *lds) {
+    const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(to) : "memory");
+}
 
-// 256 experts x 256 columns per workgroup, 8 waves of 64 x 128, two stages of
-// K = 32 in LDS: three terms of dl^T (48 KB) and NX terms of x (16 KB each),
-// both by direct loads.  x lies K-major and is read with transposing LDS reads:
-// within each 16 lanes, lane 4a + c receives element c of the 8 bytes that lanes
-// a, a+4, a+8, a+12 point at; its 16-byte piece c of row k sits at c ^ 4 (k % 4).
+// 256 experts x 256 columns per workgroup, 8 waves of 64 x 128, stages of K = 16
+// in a ring of 5 (NX = 1: three terms of dl^T, 24 KB, and x, 8 KB: 160 KB), four of
+// them in flight.  x lies K-major and is read with transposing LDS reads: within
+// each 16 lanes, lane 4a + c receives element c of the 8 bytes that lanes a, a+4,
+// a+8, a+12 point at; its 16-byte piece c of row k sits at c ^ 4 (k % 4).
 template <int NX>
 __global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, const uint16_t *__restrict__ x,
                                                   float *__restrict__ out) {
     constexpr int kA = 3 * kE * kStageK, kX = kStageK * kDwN;  // elements per stage
-    constexpr int kNStage = NX == 1 ? 2 : 1;
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[kNStage * (kA + NX * kX)];
+    constexpr int kBuf = kA + NX * kX, kRing = NX == 1 ? 5 : 3;
+    constexpr int kLoads = 3 + NX;  // per wave and stage
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[kRing * kBuf];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
@@ -319,73 +349,67 @@ __global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, c
     const int s0 = (int)((int64_t)stages * z / S), s1 = (int)((int64_t)stages * (z + 1) / S);
     out += (int64_t)z * kE * d;
 
+    // A: 24 KB in a row, 3 KB per wave; x: row 2 wave + g of each term
+    const uint16_t *asrc = ws.dlt + wave * 3 * 512 + 8 * lane;
+    const int xk = 2 * wave + g, xn = min(n0 + 8 * ((lane & 31) ^ (4 * (xk & 3))), d - 8);
     auto issue = [&](int st, uint16_t *to) {
-        const int k0 = st * kStageK;
-        // A: 48 instructions of 16 rows; 6 per wave
+        st = min(st, s1 - 1);  // behind the end the last stage again, never read: the loads stay countable
 #pragma unroll
-        for (int i = 0; i < 6; ++i) {
-            const int blk = wave * 6 + i, r = 16 * blk + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
-            dma16(ws.dlt + (int64_t)r * ws.Tp + k0 + 8 * c, to + blk * 16 * kStageK);
-        }
-        // x: NX * 16 instructions of 2 rows; 2 NX per wave
+        for (int i = 0; i < 3; ++i)
+            dma16_unseen(asrc + (int64_t)st * kA + i * 512, to + (wave * 3 + i) * 512);
+        const int64_t t = min(st * kStageK + xk, T - 1);
 #pragma unroll
-        for (int i = 0; i < 2 * NX; ++i) {
-            const int blk = wave * 2 * NX + i, r = 2 * blk + g, k = r & (kStageK - 1);
-            const int t = min(k0 + k, T - 1), n = min(n0 + 8 * ((lane & 31) ^ (4 * (k & 3))), d - 8);
-            dma16(x + ((int64_t)(r / kStageK) * T + t) * d + n, to + kA + 2 * blk * kDwN);
-        }
+        for (int u = 0; u < NX; ++u)
+            dma16_unseen(x + (u * (int64_t)T + t) * d + xn, to + kA + u * kX + 2 * wave * kDwN);
     };
     f32x16 acc[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    const int h = lane >> 4, b = lane & 15;
+    const int bk = 8 * (h >> 1) + (b >> 2);  // + 4 for the second read
     auto step = [&](const uint16_t *st) {
+        bf16x8 a[3][2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 a[3][2];
+        for (int m = 0; m < 3; ++m)
 #pragma unroll
-            for (int m = 0; m < 3; ++m)
+            for (int i = 0; i < 2; ++i)
+                a[m][i] = *reinterpret_cast<const bf16x8 *>(st + m * kE * kStageK +
+                                                            piece32(wm * 64 + 32 * i + (lane & 31), g));
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    a[m][i] = *reinterpret_cast<const bf16x8 *>(
-                        st + piece64(m * kE + wm * 64 + 32 * i + (lane & 31), 2 * ks + g));
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int u = 0; u < NX; ++u) {
+                const int col = wn * 128 + 32 * j + 16 * (h & 1) + 4 * (b & 3);
+                const uint16_t *p = st + kA + u * kX + bk * kDwN + ((((col >> 3) ^ (4 * (bk & 3))) << 3) | (col & 7));
+                const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)p);
+                const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(p + 4 * kDwN));
+                const bf16x8 xb = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-                for (int u = 0; u < NX; ++u) {
-                    const int h = lane >> 4, b = lane & 15;
-                    const int k = 16 * ks + 8 * (h >> 1) + (b >> 2);
-                    const int col = wn * 128 + 32 * j + 16 * (h & 1) + 4 * (b & 3);
-                    const uint16_t *p = st + kA + u * kX + k * kDwN + ((((col >> 3) ^ (4 * (k & 3))) << 3) | (col & 7));
-                    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)p);
-                    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(p + 4 * kDwN));
-                    const bf16x8 xb =
-                        __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                for (int m = 2 - u; m >= 0; --m)
 #pragma unroll
-                    for (int m = 2 - u; m >= 0; --m)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m][i], xb, acc[i][j], 0, 0, 0);
-                }
-        }
+                    for (int i = 0; i < 2; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m][i], xb, acc[i][j], 0, 0, 0);
+            }
     };
-    if (kNStage == 2) {
-        constexpr int kBuf = kA + NX * kX;
-        if (s0 < s1) issue(s0, smem);
-        for (int st = s0; st < s1; ++st) {
-            all_landed();  // stage st is there, stage st - 1 no longer read
-            if (st + 1 < s1) issue(st + 1, smem + ((st + 1 - s0) & 1) * kBuf);
-            step(smem + ((st - s0) & 1) * kBuf);
-        }
-    } else {
-        for (int st = s0; st < s1; ++st) {
-            issue(st, smem);
-            all_landed();
-            step(smem);
-            all_landed();
-        }
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) issue(s0 + i, smem + i * kBuf);
+    int at = 0, next = kRing - 1;
+    for (int st = s0; st < s1; ++st) {
+        // all but the youngest kRing - 2 stages of this wave's loads have landed; behind the
+        // barrier every wave's, and the stage before is no longer read
+        constexpr int kLeft = kLoads * (kRing - 2);
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_s_waitcnt((kLeft & 15) | (7 << 4) | (15 << 8) | ((kLeft >> 4) << 14));
+        __builtin_amdgcn_s_barrier();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        issue(st + kRing - 1, smem + next * kBuf);
+        step(smem + at * kBuf);
+        at = at == kRing - 1 ? 0 : at + 1;
+        next = next == kRing - 1 ? 0 : next + 1;
     }
+    all_landed();  // nothing is on its way into LDS when the workgroup ends
     // lane: column n0 + 128 wn + 32 j + lane % 32, experts 64 wm + 32 i + 8 q + 4 g + r
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -427,7 +451,7 @@ hipError_t launch_router_grad(const RouterGradArgs &a, void *workspace, hipStrea
     // dx: about one workgroup per CU, at least one round of 8 chunks each
     const int ntile = (d + kDxN - 1) / kDxN, rounds = (T + 255) / 256;
     const int S = 256 / ntile < 1 ? 1 : 256 / ntile > rounds ? rounds : 256 / ntile;
-    hipLaunchKernelGGL(k_rg_dx, dim3(S, ntile), dim3(512), 0, s, T, d, ws, a.dx_in, a.dx);
+    hipLaunchKernelGGL(k_rg_dx, dim3(S, ntile), dim3(512), 0, s, T, d, ws, ws.er, a.dx_in, a.dx);
     float *out = ws.S == 1 ? a.dw : ws.part;
     const dim3 grid((unsigned)(ws.S * ((d + kDwN - 1) / kDwN)));
     if (a.x_bf16)
