@@ -65,7 +65,7 @@ __device__ __forceinline__ void split_bf16(float v, uint32_t (&t)[3]) {
 // Position of 16-byte piece c of row r in the dw product's A tiles, rows of 32
 // bytes: eight rows that are read together lie in different banks.
 constexpr int kStageK = 16;  // K per stage of the dw product
-__device__ __forceinline__ int piece32(int r, int c) { return r * kStageK + ((c ^ ((r >> 2) & 1)) * 8); }
+__device__ __forceinline__ int piece32(int r, int c) { return r * kStageK + ((c ^ ((r >> 3) & 1)) * 8); }
 
 struct RgWs {
     uint16_t *dlh;   // [2][T][256] fp16 terms of the scaled rows of dl
@@ -208,7 +208,7 @@ constexpr int kDxN = 128;  // columns per workgroup
 
 // Position of 16-byte piece c of row r in an LDS tile of 512-byte rows: rows
 // that are read together lie in different banks.
-__device__ __forceinline__ int piece512(int r, int c) { return r * kE + ((c ^ (r & 7) ^ ((r >> 3) & 1)) * 8); }
+__device__ __forceinline__ int piece512(int r, int c) { return r * kE + ((c ^ (r & 15)) * 8); }
 
 // A workgroup keeps its 128 columns' terms of w in LDS (128 KB) and its 8 waves
 // walk 32-token chunks: their dl terms come straight from memory (each wave
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int r = 2 * (wave * 16 + i) + g, n = min(n0 + (r & (kDxN - 1)), d - 1);
-        const int c = (lane & 31) ^ (r & 7) ^ ((r >> 3) & 1);
+        const int c = (lane & 31) ^ (r & 15);
         dma16(ws.wh + ((int64_t)(r / kDxN) * d + n) * kE + 8 * c, sw + 2 * (wave * 16 + i) * kE);
     }
     const int chunks = (T + 31) / 32, S = gridDim.x, z = blockIdx.x;
@@ -283,13 +283,18 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
         if (dx_in == nullptr) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) in[j] = f32x16{};
+        } else if (whole) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) in[j][i] = dx_in[at0 + (int64_t)(8 * (i >> 2) + (i & 3)) * d + 32 * j];
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int row = 8 * (i >> 2) + (i & 3);
-                    in[j][i] = whole || (t0 + row < T && n + 32 * j < d) ? dx_in[at0 + (int64_t)row * d + 32 * j] : 0.f;
+                    in[j][i] = t0 + row < T && n + 32 * j < d ? dx_in[at0 + (int64_t)row * d + 32 * j] : 0.f;
                 }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -307,11 +312,22 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
                 const int lo = er[ch * 32 + 8 * q + r], hi = er[ch * 32 + 8 * q + 4 + r];  // wave-uniform
                 const int e = g ? hi : lo;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float v = ldexpf(acc[j][4 * q + r], e + ec[j]) + in[j][4 * q + r];
-                    if (whole || (t0 + 8 * q + r < T && n + 32 * j < d)) dx[at0 + (int64_t)(8 * q + r) * d + 32 * j] = v;
-                }
+                for (int j = 0; j < 4; ++j) acc[j][4 * q + r] = ldexpf(acc[j][4 * q + r], e + ec[j]) + in[j][4 * q + r];
             }
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dx[at0 + (int64_t)(8 * (i >> 2) + (i & 3)) * d + 32 * j] = acc[j][i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = 8 * (i >> 2) + (i & 3);
+                    if (t0 + row < T && n + 32 * j < d) dx[at0 + (int64_t)row * d + 32 * j] = acc[j][i];
+                }
+        }
     }
 }
 
