@@ -68,7 +68,8 @@ constexpr int kStageK = 16;  // K per stage of the dw product
 __device__ __forceinline__ int piece32(int r, int c) { return r * kStageK + ((c ^ ((r >> 3) & 1)) * 8); }
 
 struct RgWs {
-    uint16_t *dlh;   // [2][T][256] fp16 terms of the scaled rows of dl
+    uint16_t *dlh;   // [Tp/32][2][16][64][8] fp16 terms of the scaled rows of dl, as dx's fragments: 32 rows,
+                     // term, 16 of K, lane, 8 values; zeros behind T
     int32_t *er;     // [T] their exponents
     uint16_t *wh;    // [2][d][256] fp16 terms of the scaled columns of w
     int32_t *ec;     // [d]
@@ -100,7 +101,7 @@ RgWs carve(char *base, int T, int d, bool x_bf16) {
     };
     w.Tp = (T + 31) / 32 * 32;
     w.S = dw_splits(T, d);
-    w.dlh = reinterpret_cast<uint16_t *>(take((size_t)2 * T * kE * 2));
+    w.dlh = reinterpret_cast<uint16_t *>(take((size_t)2 * w.Tp * kE * 2));
     w.er = reinterpret_cast<int32_t *>(take((size_t)w.Tp * 4));
     w.wh = reinterpret_cast<uint16_t *>(take((size_t)2 * d * kE * 2));
     w.ec = reinterpret_cast<int32_t *>(take((size_t)d * 4));
@@ -115,7 +116,8 @@ RgWs carve(char *base, int T, int d, bool x_bf16) {
 // [nw, nw + nt): 32 rows of dl each; the rest, for an fp32 x: 1024 of its values.
 __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, const float *__restrict__ w,
                                                   const float *__restrict__ dl, const float *__restrict__ x, RgWs ws) {
-    __shared__ float tile[32][kE];
+    __shared__ float tile[32][kE + 4];
+    __shared__ int row_exp[32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if ((int)blockIdx.x < nw) {
         // thread: column n, experts 64 wave .. +63
@@ -172,17 +174,31 @@ __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
         for (int s = 32; s >= 1; s >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, s, kWave));
-        const int e = scale_exp(m);
-        if (lane == 0) ws.er[t] = -e;
-        if (t >= T) continue;
-        uint32_t h[4], q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split_f16(ldexpf(v[i], e), h[i], q[i]);
-        uint16_t *o = ws.dlh + (int64_t)t * kE + 4 * lane;
-        *reinterpret_cast<uint2 *>(o) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-        *reinterpret_cast<uint2 *>(o + (int64_t)T * kE) = uint2{q[0] | (q[1] << 16), q[2] | (q[3] << 16)};
+        if (lane == 0) {
+            row_exp[r] = scale_exp(m);
+            ws.er[t] = -row_exp[r];
+        }
     }
     __syncthreads();
+    // thread: 8 experts of a row, the 16 bytes of one lane of a fragment
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int at = c * 256 + tid, m = at & 31, k = 8 * (at >> 5), e = row_exp[m];
+        const f32x4 v0 = *reinterpret_cast<const f32x4 *>(&tile[m][k]);
+        const f32x4 v1 = *reinterpret_cast<const f32x4 *>(&tile[m][k + 4]);
+        i32x4 hi, mid;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h0, m0, h1, m1;
+            split_f16(ldexpf(i < 2 ? v0[2 * i] : v1[2 * i - 4], e), h0, m0);
+            split_f16(ldexpf(i < 2 ? v0[2 * i + 1] : v1[2 * i - 3], e), h1, m1);
+            hi[i] = (int)(h0 | (h1 << 16));
+            mid[i] = (int)(m0 | (m1 << 16));
+        }
+        uint16_t *o = ws.dlh + (int64_t)(t0 / 32) * 2 * 32 * kE + at * 8;
+        *reinterpret_cast<i32x4 *>(o) = hi;
+        *reinterpret_cast<i32x4 *>(o + 32 * kE) = mid;
+    }
     // thread: expert tid, its 32 tokens in a row
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -212,8 +228,8 @@ __device__ __forceinline__ int piece512(int r, int c) { return r * kE + ((c ^ (r
 
 // A workgroup keeps its 128 columns' terms of w in LDS (128 KB) and its 8 waves
 // walk 32-token chunks: their dl terms come straight from memory (each wave
-// has its own rows, so LDS would not save a read), there is no barrier in the
-// loop.  32x32x16 tiles, 4 per wave; lane: column n, so a store is 128 bytes of a row.
+// has its own rows, so LDS would not save a read), laid out so that a fragment is
+// 1 KB in a row; there is no barrier in the loop.  32x32x16 tiles, 4 per wave; lane: column n, so a store is 128 bytes of a row.
 __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, const int32_t *__restrict__ er,
                                                   const float *dx_in, float *dx) {
     __shared__ __attribute__((aligned(1024))) uint16_t sw[2 * kDxN * kE];
@@ -237,11 +253,11 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
     const uint32_t row_off = (uint32_t)piece512(lane & 31, g);
     f16x8 a[2][2][4];  // quarter of K (even, odd), term, step
     auto load = [&](int ch, int q, f16x8 (&v)[2][4]) {
-        const uint16_t *p = ws.dlh + (int64_t)min(ch * 32 + (lane & 31), T - 1) * kE + 8 * g + 64 * q;
+        const uint16_t *p = ws.dlh + (int64_t)ch * 2 * 32 * kE + q * 4 * 512 + 8 * lane;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            v[0][s] = *reinterpret_cast<const f16x8 *>(p + 16 * s);
-            v[1][s] = *reinterpret_cast<const f16x8 *>(p + (int64_t)T * kE + 16 * s);
+            v[0][s] = *reinterpret_cast<const f16x8 *>(p + s * 512);
+            v[1][s] = *reinterpret_cast<const f16x8 *>(p + 32 * kE + s * 512);
         }
     };
     f32x16 acc[4];
