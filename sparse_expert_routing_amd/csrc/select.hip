@@ -1,7 +1,6 @@
 // Expert choice from router logits, its gradient, and the sequence-wise balance
 // loss.
 //
-// One wave per token; lane l holds the experts l, l + 64, ... of the row.
 //   scores   s = sigmoid(l) or softmax(l) over the row
 //   choice   a = s + bias (the bias steers the choice only); the experts are
 //            cut into groups, the best groups by max or top-two sum of a stay
@@ -11,6 +10,11 @@
 // score's rounding would decide them differently from one exp to the next.
 // Without a bias the order of the scores is the order of the logits, so the
 // logits themselves are compared and nothing is rounded.
+//
+// k_select (one wave per token, lane l holds the experts l, l + 64, ...) computes
+// every score in 64 bits.  k_select_fast (16 lanes per token) chooses by fp32
+// scores, whose error it knows, and hands a token to the 64-bit code where the
+// border between chosen and not, of experts or of groups, is nearer than that.
 #include "device.h"
 #include "kernels.h"
 
@@ -214,6 +218,301 @@ __global__ __launch_bounds__(256) void k_select(SelectRule r, int T, const void 
     for (int q = 0; q < Q; ++q) l[q] = lane + 64 * q < r.E ? load_logit<BF16>(row, lane + 64 * q) : -INFINITY;
     const uint32_t chosen = choose64<Q>(r, l, bias, score64[wave], open[wave]);
     store_choice<Q>(r, t, chosen, l, idx, wts);
+}
+
+// -------------------------------------------------------- sixteen lanes per token
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) { return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v))); }
+// v of the lane N below in its row of 16, 0 for the first N.
+template <int N>
+__device__ __forceinline__ uint32_t row_shr(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x110 + N, 0xf, 0xf, true);
+}
+
+// Partner exchanges that combine 2, 4, 8, 16 neighbouring lanes when applied in
+// this order (the mirrors meet lanes that already hold their half's result).
+#define MOE_ROW_STEPS(STEP) STEP(0xB1) STEP(0x4E) STEP(0x141) STEP(0x140)
+
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#define STEP(C) v = max(v, dpp_u32<C>(v));
+    MOE_ROW_STEPS(STEP)
+#undef STEP
+    return v;
+}
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+#define STEP(C) v = min(v, dpp_u32<C>(v));
+    MOE_ROW_STEPS(STEP)
+#undef STEP
+    return v;
+}
+__device__ __forceinline__ uint32_t row_add(uint32_t v) {
+#define STEP(C) v += dpp_u32<C>(v);
+    MOE_ROW_STEPS(STEP)
+#undef STEP
+    return v;
+}
+__device__ __forceinline__ float row_sum(float v) {
+#define STEP(C) v += dpp_f32<C>(v);
+    MOE_ROW_STEPS(STEP)
+#undef STEP
+    return v;
+}
+__device__ __forceinline__ float row_maxf(float v) {
+#define STEP(C) v = fmaxf(v, dpp_f32<C>(v));
+    MOE_ROW_STEPS(STEP)
+#undef STEP
+    return v;
+}
+
+// Lanes of the row whose v is larger than this lane's.
+__device__ __forceinline__ int row_rank(uint32_t v) {
+    int n = 0;
+#define ROR(N) n += dpp_u32<0x120 + N>(v) > v;
+    ROR(1) ROR(2) ROR(3) ROR(4) ROR(5) ROR(6) ROR(7) ROR(8) ROR(9) ROR(10) ROR(11) ROR(12) ROR(13) ROR(14) ROR(15)
+#undef ROR
+    return n;
+}
+
+// 31-bit ordered key of a float (its last mantissa bit goes), 1 at least.
+__device__ __forceinline__ uint32_t key31(float v) { return (f32_order_key(v + 0.f) >> 1) | (v == -INFINITY); }
+__device__ __forceinline__ float from_key31(uint32_t k) { return f32_from_order_key(k << 1); }
+
+__device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(1.4426950408889634f * v); }
+
+// What the keys are made of: bf16 logits with the id in the low bits (no two
+// alike, nothing rounded), fp32 logits, or the biased fp32 scores.
+enum { KEY_BF16 = 0, KEY_F32 = 1, KEY_SCORE = 2 };
+
+// Sixteen lanes per token, four tokens per wave; lane i holds the Q experts from
+// Q i on.  Keys are 31-bit unsigned numbers (0: not an expert, or its group is
+// closed), so that with the largest key below m wanted, k - m as an unsigned
+// number is at least 2^31 for a key below m and less for the others, and the
+// largest difference is the answer: one subtraction and half a three-way maximum
+// per key and round, four exchanges, k + 1 rounds.
+//
+// fp32 scores: exp2 and reciprocal are off by one unit each, the exponent's
+// rounding moves a sigmoid by at most s (1 - s) |l| 2^-24 < 2^-26, a softmax by p x
+// 2^-24 with p x < 0.37 besides its sum's 30 roundings, the bias's addition and
+// the key's lost bit by 2^-23 of the sum.  Two neighbours are in doubt when they
+// are nearer than 2^-20 (sigmoid) or 2^-17 (softmax) plus 2^-21 of their size: twice
+// those errors with room.  That is also where equal keys end up.
+//
+// 16384 tokens, 256 experts in 8 groups, 8 chosen: see launch_select.
+template <int Q, int KEY, bool BF16>
+__global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per_group, bool vec, int T,
+                                                     const void *__restrict__ logits, int64_t ld,
+                                                     const float *__restrict__ bias, int32_t *__restrict__ idx,
+                                                     float *__restrict__ wts) {
+    constexpr int QS = Q / 4;  // experts per lane in the 64-bit code
+    __shared__ double score64[4][64 * QS];
+    __shared__ uint8_t open64[4][64 * QS];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15;
+    const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
+    if (t0 >= T) return;
+    const int64_t t = min(t0 + (lane >> 4), (int64_t)T - 1);
+    const bool mine = t0 + (lane >> 4) < T;
+    const int e0 = sub * Q;
+    float l[Q];
+    const char *row = static_cast<const char *>(logits) + (t * ld + e0) * (BF16 ? 2 : 4);
+    if (vec) {  // rows and lanes begin at 16 bytes, and E is a multiple of Q
+#pragma unroll
+        for (int q = 0; q < Q; ++q) l[q] = -INFINITY;
+        if (e0 < r.E) {
+            if (BF16) {
+                constexpr int W = Q >= 8 ? 8 : 4;
+#pragma unroll
+                for (int c = 0; c < Q; c += W) {
+                    uint32_t w[W / 2];
+                    if (W == 8) {
+                        const i32x4 v = *reinterpret_cast<const i32x4 *>(row + 2 * c);
+#pragma unroll
+                        for (int i = 0; i < W / 2; ++i) w[i] = (uint32_t)v[i];
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(row + 2 * c);
+                        w[0] = v.x;
+                        w[1] = v.y;
+                    }
+#pragma unroll
+                    for (int i = 0; i < W / 2; ++i) {
+                        l[c + 2 * i] = bf16_to_f32(w[i] & 0xffffu);
+                        l[c + 2 * i + 1] = bf16_to_f32(w[i] >> 16);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < Q; c += 4) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(row + 4 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) l[c + i] = v[i];
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) l[q] = e0 + q < r.E ? load_logit<BF16>(row, q) : -INFINITY;
+    }
+    // a NaN ranks behind every number: the 64-bit code's business
+    bool doubt = false;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) doubt |= l[q] != l[q];
+
+    float s[Q], total = 0.f, m = 0.f;
+    const bool scores = KEY == KEY_SCORE || (r.topk_group < r.n_group && r.top_two) || (r.softmax && !r.renorm);
+    if (r.softmax) {
+        m = l[0];
+#pragma unroll
+        for (int q = 1; q < Q; ++q) m = fmaxf(m, l[q]);
+        m = row_maxf(m);
+        doubt |= !(fabsf(m) < INFINITY);
+    }
+    if (scores) {
+        if (r.softmax) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                s[q] = fast_exp(l[q] - m);
+                total += s[q];
+            }
+            total = row_sum(total);
+            const float inv = 1.0f / total;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) s[q] *= inv;
+        } else {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) s[q] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[q]));
+        }
+    }
+    uint32_t key[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        if (KEY == KEY_SCORE) {
+            s[q] += e0 + q < r.E ? bias[e0 + q] : 0.f;
+            doubt |= s[q] != s[q];
+            key[q] = key31(s[q]);
+        } else if (KEY == KEY_F32) {
+            key[q] = key31(l[q]);
+        } else {
+            key[q] = ((f32_order_key(l[q] + 0.f) >> 16) << 15) | (uint32_t)(0x7fff - (e0 + q));
+        }
+        if (e0 + q >= r.E) key[q] = 0;
+    }
+    const float near = r.softmax ? 7.62939453125e-6f : 9.5367431640625e-7f;  // 2^-17, 2^-20
+
+    if (r.topk_group < r.n_group) {
+        uint32_t g;
+        const bool rounded = KEY == KEY_SCORE || r.top_two;
+        if (r.top_two) {
+            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const float v = e0 + q < r.E ? s[q] : -INFINITY;
+                b = fmaxf(b, fminf(a, v));
+                a = fmaxf(a, v);
+            }
+#define STEP(C, LANES)                                       \
+    if (lanes_per_group >= LANES) {                          \
+        const float oa = dpp_f32<C>(a), ob = dpp_f32<C>(b);  \
+        b = fmaxf(fminf(a, oa), fmaxf(b, ob));               \
+        a = fmaxf(a, oa);                                    \
+    }
+            STEP(0xB1, 2) STEP(0x4E, 4) STEP(0x141, 8) STEP(0x140, 16)
+#undef STEP
+            doubt |= a + b != a + b;
+            g = e0 < r.E ? key31(a + b) : 0;
+        } else {
+            g = key[0];
+#pragma unroll
+            for (int q = 1; q < Q; ++q) g = max(g, key[q]);
+#define STEP(C, LANES) \
+    if (lanes_per_group >= LANES) g = max(g, dpp_u32<C>(g));
+            STEP(0xB1, 2) STEP(0x4E, 4) STEP(0x141, 8) STEP(0x140, 16)
+#undef STEP
+        }
+        const int want = r.topk_group * lanes_per_group;
+        const bool is_open = row_rank(g) < want;
+        // equal groups at the border open together
+        doubt |= row_add(is_open ? 1u : 0u) != (uint32_t)want;
+        if (rounded) {
+            const uint32_t lo = row_min(is_open ? g : 0x7fffffffu), hi = row_max(is_open ? 0u : g);
+            const float x = from_key31(lo), y = hi ? from_key31(hi) : -INFINITY;
+            doubt |= !(x - y > 2.f * (near + 4.76837158203125e-7f * fabsf(x)));
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) key[q] = is_open ? key[q] : 0;
+    }
+
+    uint32_t at = 0x80000000u, kth = 0;
+    const int rounds = KEY == KEY_SCORE ? r.k + 1 : r.k;
+    for (int i = 0; i < rounds; ++i) {
+        uint32_t d = key[0] - at;
+#pragma unroll
+        for (int q = 1; q < Q; ++q) d = max(d, key[q] - at);
+        d = row_max(d);
+        if (i == r.k - 1) kth = at + d;
+        // none below: nothing (0) from here on
+        at = d >= 0x80000000u ? at + d : 0;
+    }
+    if (KEY == KEY_SCORE) {
+        const float x = from_key31(kth), y = at ? from_key31(at) : -INFINITY;
+        doubt |= !(x - y > near + 4.76837158203125e-7f * fabsf(x));
+    }
+    // bit Q - 1 - q: expert e0 + q is chosen
+    uint32_t chosen = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) chosen = __builtin_amdgcn_alignbit(chosen, (kth - 1u) - key[q], 31);
+    const uint32_t count = __popc(chosen);
+    doubt |= row_add(count) != (uint32_t)r.k || kth <= 1u || kth >= 0x80000000u;
+
+    // the chosen scores and their sum
+    float sum = 0.f;
+    if (r.softmax && r.renorm) {
+        // relative to the largest chosen
+        float mc = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) mc = fmaxf(mc, (chosen >> (Q - 1 - q)) & 1 ? l[q] : -INFINITY);
+        m = row_maxf(mc);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        if ((chosen >> (Q - 1 - q)) & 1) {
+            s[q] = r.softmax ? expf(l[q] - m) : sigmoid_f32(l[q]);
+            sum += s[q];
+        }
+    }
+    sum = r.renorm ? row_sum(sum) : r.softmax ? total : 1.f;
+    uint32_t pos = count;
+    pos += row_shr<1>(pos);
+    pos += row_shr<2>(pos);
+    pos += row_shr<4>(pos);
+    pos += row_shr<8>(pos);
+    pos -= count;
+    doubt = row_add(doubt ? 1u : 0u) != 0;
+    if (mine && !doubt) {
+        int64_t o = t * r.k + pos;
+        const float c = sum == 0.f ? 0.f : r.scale / sum;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if ((chosen >> (Q - 1 - q)) & 1) {
+                idx[o] = e0 + q;
+                wts[o] = s[q] * c;
+                ++o;
+            }
+    }
+    // the tokens in doubt, one after the other, in 64 bits
+    const uint64_t left = __ballot(mine && doubt);
+    for (int i = 0; i < 4; ++i) {
+        if (!((left >> (16 * i)) & 1)) continue;
+        const void *rw = static_cast<const char *>(logits) + (t0 + i) * ld * (BF16 ? 2 : 4);
+        float v[QS];
+#pragma unroll
+        for (int q = 0; q < QS; ++q) v[q] = lane + 64 * q < r.E ? load_logit<BF16>(rw, lane + 64 * q) : -INFINITY;
+        const uint32_t c = choose64<QS>(r, v, bias, score64[wave], open64[wave]);
+        store_choice<QS>(r, t0 + i, c, v, idx, wts);
+    }
 }
 
 // ------------------------------------------------------------- the sequences
@@ -420,8 +719,42 @@ int balance_blocks(int T) { return (T + kBalanceTokens - 1) / kBalanceTokens; }
         else LAUNCH(16);                           \
     } while (0)
 
+// Lanes per group of k_select_fast<Q>, 0 where its exchanges do not fit the
+// groups: a group has to be 1, 2, 4, 8 or 16 whole lanes.
+static int group_lanes(const SelectRule &r, int Q) {
+    if (r.topk_group == r.n_group) return 16;  // no group is closed
+    const int per = r.E / r.n_group, n = per / Q;
+    return per % Q == 0 && n <= 16 && (n & (n - 1)) == 0 ? n : 0;
+}
+
 hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)a.T + 3) / 4)), block(256);
+    const SelectRule &r = a.rule;
+    const dim3 block(256);
+    const int Q = r.E <= 64 ? 4 : r.E <= 128 ? 8 : r.E <= 256 ? 16 : 32;
+    const int lanes = r.E <= 512 ? group_lanes(r, Q) : 0;
+    if (lanes) {
+        const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16));
+        const int64_t bytes = a.bf16 ? 2 : 4, step = Q * bytes < 16 ? Q * bytes : 16;
+        const bool vec = r.E % Q == 0 && reinterpret_cast<uintptr_t>(a.logits) % step == 0 && a.ld * bytes % step == 0;
+#define FAST(QQ)                                                                                                     \
+    do {                                                                                                             \
+        if (a.bias && a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, true>), grid, block, 0, s, r, lanes,   \
+                                                 vec, a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                \
+        else if (a.bias) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, false>), grid, block, 0, s, r, lanes, vec, \
+                                            a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                          \
+        else if (a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_BF16, true>), grid, block, 0, s, r, lanes, vec,   \
+                                            a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                          \
+        else hipLaunchKernelGGL((k_select_fast<QQ, KEY_F32, false>), grid, block, 0, s, r, lanes, vec, a.T, a.logits, \
+                                a.ld, a.bias, a.idx, a.weights);                                                     \
+    } while (0)
+        if (Q == 4) FAST(4);
+        else if (Q == 8) FAST(8);
+        else if (Q == 16) FAST(16);
+        else FAST(32);
+#undef FAST
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)(((int64_t)a.T + 3) / 4));
 #define GO(Q)                                                                                                        \
     do {                                                                                                             \
         if (a.bf16) hipLaunchKernelGGL((k_select<Q, true>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld, a.bias,   \
