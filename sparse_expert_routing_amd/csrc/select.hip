@@ -309,7 +309,7 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
                                                      const float *__restrict__ bias, int32_t *__restrict__ idx,
                                                      float *__restrict__ wts) {
     constexpr int QS = Q / 4;  // experts per lane in the 64-bit code
-    __shared__ double score64[4][64 * QS];
+    __shared__ __attribute__((aligned(16))) float sc[4][64 * Q];  // the scores; 64-bit ones in the 64-bit code
     __shared__ uint8_t open64[4][64 * QS];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15;
     const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
@@ -317,12 +317,20 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
     const int64_t t = min(t0 + (lane >> 4), (int64_t)T - 1);
     const bool mine = t0 + (lane >> 4) < T;
     const int e0 = sub * Q;
-    float l[Q];
-    const char *row = static_cast<const char *>(logits) + (t * ld + e0) * (BF16 ? 2 : 4);
-    if (vec) {  // rows and lanes begin at 16 bytes, and E is a multiple of Q
+    float l[Q], b[Q];
+    // a lane behind the last expert loads what lane 0 does
+    const int first = e0 < r.E ? e0 : 0;
+    const char *row = static_cast<const char *>(logits) + (t * ld + first) * (BF16 ? 2 : 4);
+    if (vec) {  // rows, bias and lanes begin at 16 bytes, and E is a multiple of Q
+        {
+            if (KEY == KEY_SCORE) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) l[q] = -INFINITY;
-        if (e0 < r.E) {
+                for (int c = 0; c < Q; c += 4) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(bias + first + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b[c + i] = v[i];
+                }
+            }
             if (BF16) {
                 constexpr int W = Q >= 8 ? 8 : 4;
 #pragma unroll
@@ -354,51 +362,53 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) l[q] = e0 + q < r.E ? load_logit<BF16>(row, q) : -INFINITY;
+        for (int q = 0; q < Q; ++q) l[q] = load_logit<BF16>(row, min(first + q, r.E - 1) - first);
+        if (KEY == KEY_SCORE) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) b[q] = bias[min(first + q, r.E - 1)];
+        }
     }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) l[q] = e0 + q < r.E ? l[q] : -INFINITY;
     // a NaN ranks behind every number: the 64-bit code's business
     bool doubt = false;
 #pragma unroll
     for (int q = 0; q < Q; ++q) doubt |= l[q] != l[q];
 
-    float s[Q], total = 0.f, m = 0.f;
-    const bool scores = KEY == KEY_SCORE || (r.topk_group < r.n_group && r.top_two) || (r.softmax && !r.renorm);
+    float s[Q], total = 1.f, m = 0.f;
     if (r.softmax) {
         m = l[0];
 #pragma unroll
         for (int q = 1; q < Q; ++q) m = fmaxf(m, l[q]);
         m = row_maxf(m);
         doubt |= !(fabsf(m) < INFINITY);
-    }
-    if (scores) {
-        if (r.softmax) {
+        total = 0.f;
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                s[q] = fast_exp(l[q] - m);
-                total += s[q];
-            }
-            total = row_sum(total);
-            const float inv = 1.0f / total;
-#pragma unroll
-            for (int q = 0; q < Q; ++q) s[q] *= inv;
-        } else {
-#pragma unroll
-            for (int q = 0; q < Q; ++q) s[q] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[q]));
+        for (int q = 0; q < Q; ++q) {
+            s[q] = fast_exp(l[q] - m);
+            total += s[q];
         }
+        total = row_sum(total);
+        const float inv = 1.0f / total;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) s[q] *= inv;
+    } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) s[q] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[q]));
     }
     uint32_t key[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         if (KEY == KEY_SCORE) {
-            s[q] += e0 + q < r.E ? bias[e0 + q] : 0.f;
-            doubt |= s[q] != s[q];
-            key[q] = key31(s[q]);
+            b[q] += s[q];
+            doubt |= b[q] != b[q];
+            key[q] = key31(b[q]);
         } else if (KEY == KEY_F32) {
             key[q] = key31(l[q]);
         } else {
             key[q] = ((f32_order_key(l[q] + 0.f) >> 16) << 15) | (uint32_t)(0x7fff - (e0 + q));
         }
-        if (e0 + q >= r.E) key[q] = 0;
+        key[q] = e0 + q < r.E ? key[q] : 0;
     }
     const float near = r.softmax ? 7.62939453125e-6f : 9.5367431640625e-7f;  // 2^-17, 2^-20
 
@@ -406,23 +416,23 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
         uint32_t g;
         const bool rounded = KEY == KEY_SCORE || r.top_two;
         if (r.top_two) {
-            float a = -INFINITY, b = -INFINITY;
+            float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                const float v = e0 + q < r.E ? s[q] : -INFINITY;
-                b = fmaxf(b, fminf(a, v));
-                a = fmaxf(a, v);
+                const float v = KEY == KEY_SCORE ? b[q] : s[q];
+                a2 = __builtin_amdgcn_fmed3f(a1, a2, v);  // a2 <= a1: the second of the three
+                a1 = fmaxf(a1, v);
             }
-#define STEP(C, LANES)                                       \
-    if (lanes_per_group >= LANES) {                          \
-        const float oa = dpp_f32<C>(a), ob = dpp_f32<C>(b);  \
-        b = fmaxf(fminf(a, oa), fmaxf(b, ob));               \
-        a = fmaxf(a, oa);                                    \
+#define STEP(C, LANES)                                         \
+    if (lanes_per_group >= LANES) {                            \
+        const float o1 = dpp_f32<C>(a1), o2 = dpp_f32<C>(a2);  \
+        a2 = fmaxf(fminf(a1, o1), fmaxf(a2, o2));              \
+        a1 = fmaxf(a1, o1);                                    \
     }
             STEP(0xB1, 2) STEP(0x4E, 4) STEP(0x141, 8) STEP(0x140, 16)
 #undef STEP
-            doubt |= a + b != a + b;
-            g = e0 < r.E ? key31(a + b) : 0;
+            doubt |= a1 + a2 != a1 + a2;
+            g = e0 < r.E ? key31(a1 + a2) : 0;
         } else {
             g = key[0];
 #pragma unroll
@@ -467,23 +477,17 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
     const uint32_t count = __popc(chosen);
     doubt |= row_add(count) != (uint32_t)r.k || kth <= 1u || kth >= 0x80000000u;
 
-    // the chosen scores and their sum
+    // the chosen scores' sum; a softmax's that underflows next to the row's largest is left to
+    // the 64-bit code's way, which is relative to the largest chosen
     float sum = 0.f;
-    if (r.softmax && r.renorm) {
-        // relative to the largest chosen
-        float mc = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) mc = fmaxf(mc, (chosen >> (Q - 1 - q)) & 1 ? l[q] : -INFINITY);
-        m = row_maxf(mc);
-    }
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        if ((chosen >> (Q - 1 - q)) & 1) {
-            s[q] = r.softmax ? expf(l[q] - m) : sigmoid_f32(l[q]);
-            sum += s[q];
-        }
+        sum += (chosen >> (Q - 1 - q)) & 1 ? s[q] : 0.f;
+        sc[wave][lane * Q + q] = s[q];
     }
-    sum = r.renorm ? row_sum(sum) : r.softmax ? total : 1.f;
+    sum = row_sum(sum);
+    doubt |= r.softmax && r.renorm && !(sum > 1e-30f);
+    if (!r.renorm) sum = 1.f;
     uint32_t pos = count;
     pos += row_shr<1>(pos);
     pos += row_shr<2>(pos);
@@ -491,17 +495,19 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
     pos += row_shr<8>(pos);
     pos -= count;
     doubt = row_add(doubt ? 1u : 0u) != 0;
+    wave_sync();
     if (mine && !doubt) {
-        int64_t o = t * r.k + pos;
+        int32_t *io = idx + t * r.k + pos;
+        float *wo = wts + t * r.k + pos;
         const float c = sum == 0.f ? 0.f : r.scale / sum;
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if ((chosen >> (Q - 1 - q)) & 1) {
-                idx[o] = e0 + q;
-                wts[o] = s[q] * c;
-                ++o;
-            }
+        for (uint32_t left = chosen << (32 - Q); left != 0;) {
+            const int q = __clz(left);
+            left &= ~(0x80000000u >> q);
+            *io++ = e0 + q;
+            *wo++ = sc[wave][lane * Q + q] * c;
+        }
     }
+    wave_sync();
     // the tokens in doubt, one after the other, in 64 bits
     const uint64_t left = __ballot(mine && doubt);
     for (int i = 0; i < 4; ++i) {
@@ -510,7 +516,7 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
         float v[QS];
 #pragma unroll
         for (int q = 0; q < QS; ++q) v[q] = lane + 64 * q < r.E ? load_logit<BF16>(rw, lane + 64 * q) : -INFINITY;
-        const uint32_t c = choose64<QS>(r, v, bias, score64[wave], open64[wave]);
+        const uint32_t c = choose64<QS>(r, v, bias, reinterpret_cast<double *>(sc[wave]), open64[wave]);
         store_choice<QS>(r, t0 + i, c, v, idx, wts);
     }
 }
@@ -735,7 +741,8 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
     if (lanes) {
         const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16));
         const int64_t bytes = a.bf16 ? 2 : 4, step = Q * bytes < 16 ? Q * bytes : 16;
-        const bool vec = r.E % Q == 0 && reinterpret_cast<uintptr_t>(a.logits) % step == 0 && a.ld * bytes % step == 0;
+        const bool vec = r.E % Q == 0 && reinterpret_cast<uintptr_t>(a.logits) % step == 0 && a.ld * bytes % step == 0 &&
+                         reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
 #define FAST(QQ)                                                                                                     \
     do {                                                                                                             \
         if (a.bias && a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, true>), grid, block, 0, s, r, lanes,   \
