@@ -233,24 +233,28 @@ def _library():
     return load()
 
 
-_STORAGE = None
+_torch = None
+_KINDS = {}
 
 
-def _storage():
-    """The torch types a storage type travels in (bf16 also as its 16-bit patterns)."""
-    global _STORAGE
-    if _STORAGE is None:
-        import torch
-        _STORAGE = {MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16), MOE_E4M3: (torch.uint8,),
-                    "i32": (torch.int32,), "byte": (torch.uint8, torch.int8)}
-    return _STORAGE
+def _bind_torch():
+    global _torch
+    import torch
+    # the torch types a storage type travels in (bf16 also as its 16-bit patterns)
+    _KINDS.update({MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16), MOE_E4M3: (torch.uint8,),
+                   "i32": (torch.int32,), "byte": (torch.uint8, torch.int8)})
+    _torch = torch
 
 
 class _Call:
     """Checks of one call's tensors, which have to lie on one GPU, and its launch there."""
 
+    __slots__ = ("fn", "index", "elsewhere")
+
     def __init__(self, fn):
-        self.fn, self.device, self.elsewhere = fn, None, None
+        if _torch is None:
+            _bind_torch()
+        self.fn, self.index, self.elsewhere = fn, -1, None
 
     def refuse(self, what):
         raise MoeError(self.fn, MOE_EINVAL, "MOE_EINVAL: " + what)
@@ -261,35 +265,38 @@ class _Call:
             if not optional:
                 self.refuse(f"{name} is missing")
             return None
-        if t.dtype not in _storage()[kind]:
+        if t.dtype not in _KINDS[kind]:
             self.refuse(f"{name} has type {t.dtype}")
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
         if not t.is_contiguous():
             self.refuse(f"{name} is not contiguous")
-        return self.on(name, t)
+        if t.get_device() != self.index or not t.is_cuda:
+            self.on(name, t)
+        return t.data_ptr()
 
     def rows(self, name, t, kind, shape):
         """The address and row stride of a tensor whose rows are contiguous."""
         if t is None:
             self.refuse(f"{name} is missing")
-        if t.dtype not in _storage()[kind]:
+        if t.dtype not in _KINDS[kind]:
             self.refuse(f"{name} has type {t.dtype}")
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
-        ld = t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
-        if (shape[1] > 1 and t.stride(1) != 1) or ld < shape[1]:
+        ld, step = t.stride()
+        if shape[0] == 1:
+            ld = max(ld, shape[1])
+        if (shape[1] > 1 and step != 1) or ld < shape[1]:
             self.refuse(f"{name} has strides {tuple(t.stride())}: its rows have to be contiguous and apart")
-        return self.on(name, t), ld
+        if t.get_device() != self.index or not t.is_cuda:
+            self.on(name, t)
+        return t.data_ptr(), ld
 
     def on(self, name, t):
-        device = t.device
-        if device != self.device:
-            if self.device is None and device.type == "cuda":
-                self.device = device
-            elif self.elsewhere is None:  # reported behind the types and shapes
-                self.elsewhere = f"{name} is on {device}" + (f", not {self.device}" if self.device is not None else "")
-        return t.data_ptr()
+        if self.index < 0 and t.is_cuda:
+            self.index = t.get_device()
+        elif self.elsewhere is None:  # reported behind the types and shapes
+            self.elsewhere = f"{name} is on {t.device}" + (f", not cuda:{self.index}" if self.index >= 0 else "")
 
     def workspace(self, t):
         """Address and size of a workspace (None: none)."""
@@ -297,22 +304,27 @@ class _Call:
             return None, 0
         if not t.is_contiguous():
             self.refuse("the workspace is not contiguous")
-        return self.on("the workspace", t), t.numel() * t.element_size()
+        if t.get_device() != self.index or not t.is_cuda:
+            self.on("the workspace", t)
+        return t.data_ptr(), t.numel() * t.element_size()
 
     def run(self, call, *args, stream=None):
-        import torch
         if self.elsewhere is not None:
             self.refuse(self.elsewhere)
+        index, cuda = self.index, _torch.cuda
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        elif stream.device != self.device:
-            self.refuse(f"the stream is on {stream.device}, not {self.device}")
-        if torch.cuda.current_device() == self.device.index:
-            st = call(*args, stream.cuda_stream)
+            raw = _torch._C._cuda_getCurrentRawStream(index)
+        elif stream.device.index != index:
+            self.refuse(f"the stream is on {stream.device}, not cuda:{index}")
         else:
-            with torch.cuda.device(self.device):
-                st = call(*args, stream.cuda_stream)
-        _check(self.fn, st)
+            raw = stream.cuda_stream
+        if cuda.current_device() == index:
+            st = call(*args, raw)
+        else:
+            with cuda.device(index):
+                st = call(*args, raw)
+        if st != MOE_OK:
+            _check(self.fn, st)
 
 
 def moe_router_logits(ds, x, w_router, logits, workspace=None, stream=None):
@@ -374,7 +386,7 @@ def _plain_type(c, name, t):
     if t is None or t.dim() != 2:
         c.refuse(f"{name} has to be a matrix")
     for kind in (MOE_F32, MOE_BF16):
-        if t.dtype in _storage()[kind]:
+        if t.dtype in _KINDS[kind]:
             return kind
     c.refuse(f"{name} has type {t.dtype}")
 
