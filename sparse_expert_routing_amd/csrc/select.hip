@@ -284,6 +284,58 @@ __device__ __forceinline__ float from_key31(uint32_t k) { return f32_from_order_
 
 __device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(1.4426950408889634f * v); }
 
+// The Q experts from e0 on of a row that begins `at` elements into p, -inf behind
+// the last expert (a lane with no expert loads what lane 0 does).  vec: rows and
+// lanes begin at 16 bytes (or all of a lane's), and E is a multiple of Q.
+template <int Q, bool BF16>
+__device__ __forceinline__ void load_row(const void *p, int64_t at, int e0, int E, bool vec, float (&l)[Q]) {
+    const int first = e0 < E ? e0 : 0;
+    const char *row = static_cast<const char *>(p) + (at + first) * (BF16 ? 2 : 4);
+    if (vec && BF16) {
+        constexpr int W = Q >= 8 ? 4 : 2;  // words per load
+#pragma unroll
+        for (int c = 0; c < Q / 2; c += W) {
+            uint32_t w[4];
+            if (W == 4) {
+                const i32x4 v = *reinterpret_cast<const i32x4 *>(row + 4 * c);
+                w[0] = (uint32_t)v[0]; w[1] = (uint32_t)v[1]; w[2] = (uint32_t)v[2]; w[3] = (uint32_t)v[3];
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2 *>(row + 4 * c);
+                w[0] = v.x; w[1] = v.y;
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                l[2 * (c + i)] = bf16_to_f32(w[i] & 0xffffu);
+                l[2 * (c + i) + 1] = bf16_to_f32(w[i] >> 16);
+            }
+        }
+    } else if (vec) {
+#pragma unroll
+        for (int c = 0; c < Q; c += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(row + 4 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[c + i] = v[i];
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) l[q] = load_logit<BF16>(row, min(first + q, E - 1) - first);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) l[q] = e0 + q < E ? l[q] : -INFINITY;
+}
+template <int Q>
+__device__ __forceinline__ void load_f32(const float *p, int64_t at, int e0, int E, bool vec, float (&v)[Q]) {
+    load_row<Q, false>(p, at, e0, E, vec, v);
+}
+
+// Whether load_row can load whole vectors of rows ld apart, and of a dense fp32
+// array beside them.
+bool rows_vec(int Q, int E, bool bf16, const void *logits, int64_t ld, const void *a, const void *b = nullptr) {
+    const int64_t bytes = bf16 ? 2 : 4, step = Q * bytes < 16 ? Q * bytes : 16;
+    return E % Q == 0 && reinterpret_cast<uintptr_t>(logits) % step == 0 && ld * bytes % step == 0 &&
+           reinterpret_cast<uintptr_t>(a) % 16 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0;
+}
+
 // What the keys are made of: bf16 logits with the id in the low bits (no two
 // alike, nothing rounded), fp32 logits, or the biased fp32 scores.
 enum { KEY_BF16 = 0, KEY_F32 = 1, KEY_SCORE = 2 };
@@ -318,58 +370,8 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
     const bool mine = t0 + (lane >> 4) < T;
     const int e0 = sub * Q;
     float l[Q], b[Q];
-    // a lane behind the last expert loads what lane 0 does
-    const int first = e0 < r.E ? e0 : 0;
-    const char *row = static_cast<const char *>(logits) + (t * ld + first) * (BF16 ? 2 : 4);
-    if (vec) {  // rows, bias and lanes begin at 16 bytes, and E is a multiple of Q
-        {
-            if (KEY == KEY_SCORE) {
-#pragma unroll
-                for (int c = 0; c < Q; c += 4) {
-                    const f32x4 v = *reinterpret_cast<const f32x4 *>(bias + first + c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) b[c + i] = v[i];
-                }
-            }
-            if (BF16) {
-                constexpr int W = Q >= 8 ? 8 : 4;
-#pragma unroll
-                for (int c = 0; c < Q; c += W) {
-                    uint32_t w[W / 2];
-                    if (W == 8) {
-                        const i32x4 v = *reinterpret_cast<const i32x4 *>(row + 2 * c);
-#pragma unroll
-                        for (int i = 0; i < W / 2; ++i) w[i] = (uint32_t)v[i];
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(row + 2 * c);
-                        w[0] = v.x;
-                        w[1] = v.y;
-                    }
-#pragma unroll
-                    for (int i = 0; i < W / 2; ++i) {
-                        l[c + 2 * i] = bf16_to_f32(w[i] & 0xffffu);
-                        l[c + 2 * i + 1] = bf16_to_f32(w[i] >> 16);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < Q; c += 4) {
-                    const f32x4 v = *reinterpret_cast<const f32x4 *>(row + 4 * c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) l[c + i] = v[i];
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < Q; ++q) l[q] = load_logit<BF16>(row, min(first + q, r.E - 1) - first);
-        if (KEY == KEY_SCORE) {
-#pragma unroll
-            for (int q = 0; q < Q; ++q) b[q] = bias[min(first + q, r.E - 1)];
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < Q; ++q) l[q] = e0 + q < r.E ? l[q] : -INFINITY;
+    load_row<Q, BF16>(logits, t * ld, e0, r.E, vec, l);
+    if (KEY == KEY_SCORE) load_f32<Q>(bias, 0, e0, r.E, vec, b);
     // a NaN ranks behind every number: the 64-bit code's business
     bool doubt = false;
 #pragma unroll
@@ -549,133 +551,206 @@ __device__ __forceinline__ int sequence_of(const int32_t *__restrict__ off, int 
 //     the scores over their sum and b_e = alpha dloss load_e / tokens.
 // Written in the shares r and p' (never in ds / S), nothing overflows where a
 // row's scores are tiny; a row with no score at all has no gradient.
+//
+// Sixteen lanes per token as in k_select_fast; the chosen experts' gradients, made
+// by the lanes of their places in idx, reach their experts through LDS.  dense:
+// every logit has a gradient; else the row is not read but for the chosen.
+// Bound by memory: see launch_select_backward.
 template <int Q, bool BF16>
-__global__ __launch_bounds__(256) void k_select_backward(SelectRule r, int T, const void *__restrict__ logits,
+__global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec, int T, const void *__restrict__ logits,
                                                          int64_t ld, const int32_t *__restrict__ idx,
                                                          const float *__restrict__ dw, BalanceGrad b,
                                                          float *__restrict__ dlogits) {
-    __shared__ float acc[4][64 * Q];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-    if (t >= T) return;
-    const void *row = static_cast<const char *>(logits) + t * ld * (BF16 ? 2 : 4);
-    float l[Q], p[Q], one_minus[Q], g[Q];
-    float m = -INFINITY, total = 0.f;
+    __shared__ __attribute__((aligned(16))) float acc[4][64 * Q];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15;
+    const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
+    if (t0 >= T) return;
+    const int64_t t = min(t0 + (lane >> 4), (int64_t)T - 1);
+    const bool mine = t0 + (lane >> 4) < T;
+    const int e0 = sub * Q;
+    const bool dense = b.seq || (r.softmax && !r.renorm);
+    float p[Q], m = -INFINITY, total = 0.f;
+    float *const row_acc = &acc[wave][(lane & 48) * Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        l[q] = lane + 64 * q < r.E ? load_logit<BF16>(row, lane + 64 * q) : -INFINITY;
-        m = fmaxf(m, l[q]);
-    }
-    if (r.softmax) m = wave_max_f32(m, kWave);
+    for (int q = 0; q < Q; ++q) acc[wave][lane * Q + q] = 0.f;
+    if (dense) {
+        load_row<Q, BF16>(logits, t * ld, e0, r.E, vec, p);
+        if (r.softmax) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        p[q] = r.softmax ? softmax_term(l[q], m) : sigmoid_f32(l[q]);
-        one_minus[q] = r.softmax ? 1.f : sigmoid_f32(-l[q]);
-        total += p[q];
-        acc[wave][lane + 64 * q] = 0.f;
-    }
-    total = wave_sum_f32(total);
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        p[q] = total == 0.f ? 0.f : p[q] / total;  // shares of the whole row
-        g[q] = 0.f;
-    }
-    wave_sync();
-    if (dw) {
-        const int e = lane < r.k ? idx[t * r.k + lane] : -1;
-        const bool on = e >= 0 && e < r.E;
-        const float le = on ? load_logit<BF16>(row, e) : -INFINITY;
-        const float c = on ? r.scale * dw[t * r.k + lane] : 0.f;
-        float d = 0.f;
-        if (r.renorm) {
-            const float mc = wave_max_f32(le, kWave);
-            const float s = !on ? 0.f : r.softmax ? softmax_term(le, mc) : sigmoid_f32(le);
-            const float S = wave_sum_f32(s);
-            const float share = S == 0.f ? 0.f : s / S;
-            d = share * (c - wave_sum_f32(c * share)) * (r.softmax ? 1.f : sigmoid_f32(-le));
-        } else if (r.softmax) {
-            const float pe = on && total != 0.f ? softmax_term(le, m) / total : 0.f;
-            d = c * pe;
-            const float mean = wave_sum_f32(d);
-#pragma unroll
-            for (int q = 0; q < Q; ++q) g[q] -= p[q] * mean;
-        } else {
-            d = on ? c * sigmoid_f32(le) * sigmoid_f32(-le) : 0.f;
+            for (int q = 0; q < Q; ++q) m = fmaxf(m, p[q]);
+            m = row_maxf(m);
         }
-        if (on) acc[wave][e] = d;
+    }
+    // the balance loss's coefficients of the row's sequence
+    float f[Q], scale = 0.f;
+    if (b.seq) {
+        const int last = (int)min(t0 + 3, (int64_t)T - 1);
+        int s = sequence_of(b.seq, b.n_seq, (int)t0);
+        if (sequence_of(b.seq, b.n_seq, last) != s) {
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+                const int si = sequence_of(b.seq, b.n_seq, min((int)t0 + i, last));
+                s = (lane >> 4) >= i ? si : s;
+            }
+        }
+        const int at = min(s, b.n_seq - 1), start = b.seq[at], end = b.seq[at + 1];
+        if (s < b.n_seq && t >= start && t < end) scale = b.alpha * b.dloss[at] / (float)(end - start);
+        load_f32<Q>(b.load, (int64_t)at * r.E, e0, r.E, vec, f);
+    }
+    float mean = 0.f;  // softmax weights as they are: sum_j c dw_j p_j
+    wave_sync();
+    if (dense) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            // (a sigmoid's p keeps the logit until its share is known)
+            const float v = r.softmax ? (m == -INFINITY ? 0.f : fast_exp(p[q] - m))
+                                      : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
+            total += v;
+            if (r.softmax) p[q] = v;
+        }
+        total = row_sum(total);
+    }
+    if (dw) {
+        float d[4], share[4], le[4];
+        int e[4];
+        float mc = -INFINITY, S = 0.f, cross = 0.f;
+        const int places = (r.k + 15) / 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= places) continue;
+            const int j = 16 * i + sub;
+            e[i] = j < r.k ? idx[t * r.k + j] : -1;
+            const bool on = e[i] >= 0 && e[i] < r.E;
+            if (!on) e[i] = -1;
+            le[i] = on ? load_logit<BF16>(static_cast<const char *>(logits) + t * ld * (BF16 ? 2 : 4), e[i]) : -INFINITY;
+            d[i] = on ? r.scale * dw[t * r.k + j] : 0.f;
+            mc = fmaxf(mc, le[i]);
+        }
+        if (r.softmax) mc = r.renorm ? row_maxf(mc) : m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= places) continue;
+            share[i] = e[i] < 0 ? 0.f : r.softmax ? softmax_term(le[i], mc) : sigmoid_f32(le[i]);
+            S += share[i];
+        }
+        S = r.renorm ? row_sum(S) : r.softmax ? total : 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= places) continue;
+            share[i] = S == 0.f ? 0.f : share[i] / S;
+            cross += d[i] * share[i];
+        }
+        cross = row_sum(cross);
+        if (r.softmax && !r.renorm) mean = cross;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= places) continue;
+            d[i] = share[i] * (r.renorm ? d[i] - cross : d[i]) * (r.softmax ? 1.f : sigmoid_f32(-le[i]));
+            if (e[i] >= 0) row_acc[e[i]] = d[i];
+        }
     }
     wave_sync();
-    if (b.seq) {
-        const int n = b.n_seq, q0 = sequence_of(b.seq, n, (int)t);
-        const int start = q0 < n ? b.seq[q0] : T, end = q0 < n ? b.seq[q0 + 1] : T;
-        if (t >= start && t < end) {
-            const float c = b.alpha * b.dloss[q0] / (float)(end - start);
-            float f[Q], dot = 0.f;
+    float g[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) g[q] = acc[wave][lane * Q + q];
+    if (dense) {
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        float dot = 0.f;
+        if (b.seq) {
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                f[q] = lane + 64 * q < r.E ? c * b.load[(int64_t)q0 * r.E + lane + 64 * q] : 0.f;
-                dot += f[q] * p[q];
+                f[q] = e0 + q < r.E ? scale * f[q] : 0.f;
+                const float v = r.softmax ? p[q] : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
+                dot += f[q] * (v * inv);
             }
-            dot = wave_sum_f32(dot);
+            dot = row_sum(dot);
+        }
 #pragma unroll
-            for (int q = 0; q < Q; ++q) g[q] += p[q] * (f[q] - dot) * one_minus[q];
+        for (int q = 0; q < Q; ++q) {
+            float v = p[q], rest = 1.f;
+            if (!r.softmax) {
+                const float x = fast_exp(-p[q]);
+                v = __builtin_amdgcn_rcpf(1.0f + x);
+                rest = x > 1e30f ? 1.f : x * v;  // 1 - v
+            }
+            g[q] += v * inv * ((b.seq ? f[q] - dot : 0.f) * rest - mean);
         }
     }
+    if (!mine) return;
+    float *o = dlogits + t * r.E + e0;
+    if (vec) {
+        if (e0 < r.E) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
-        if (lane + 64 * q < r.E) dlogits[t * r.E + lane + 64 * q] = g[q] + acc[wave][lane + 64 * q];
+            for (int q = 0; q < Q; q += 4) *reinterpret_cast<f32x4 *>(o + q) = f32x4{g[q], g[q + 1], g[q + 2], g[q + 3]};
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (e0 + q < r.E) o[q] = g[q];
+    }
 }
 
 // Partial sums of the balance loss: a workgroup takes kBalanceTokens tokens and
 // walks the sequences that lie in them; each (workgroup, sequence) pair owns
 // slot workgroup + sequence (ascending in both, so no two share one), where it
 // leaves the sum of the tokens' shares and the count of choices per expert.
+// Sixteen lanes per token, each lane sums its own experts.
 template <int Q, bool BF16>
-__global__ __launch_bounds__(256) void k_balance_part(SelectRule r, int T, const void *__restrict__ logits, int64_t ld,
-                                                      const int32_t *__restrict__ idx, const int32_t *__restrict__ seq,
-                                                      int n_seq, float *__restrict__ part, int32_t *__restrict__ count) {
-    __shared__ float share[4][64 * Q];
-    __shared__ int32_t hist[64 * Q];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int t1 = min((int)min((int64_t)(blockIdx.x + 1) * kBalanceTokens, (int64_t)T), T);
+__global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, int T, const void *__restrict__ logits,
+                                                      int64_t ld, const int32_t *__restrict__ idx,
+                                                      const int32_t *__restrict__ seq, int n_seq,
+                                                      float *__restrict__ part, int32_t *__restrict__ count) {
+    __shared__ float share[8][16 * Q];
+    __shared__ int32_t hist[16 * Q];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, e0 = (lane & 15) * Q;
+    const int t1 = (int)min((int64_t)(blockIdx.x + 1) * kBalanceTokens, (int64_t)T);
     int t = max((int)((int64_t)blockIdx.x * kBalanceTokens), seq[0]);
     while (t < t1) {
         const int s = sequence_of(seq, n_seq, t);
         if (s >= n_seq) break;
         const int end = max(t + 1, min(t1, seq[s + 1]));
-        for (int e = tid; e < 64 * Q; e += 256) hist[e] = 0;
+        for (int e = tid; e < 16 * Q; e += 512) hist[e] = 0;
         float sum[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q) sum[q] = 0.f;
-        for (int u = t + wave; u < end; u += 4) {
-            const void *row = static_cast<const char *>(logits) + (int64_t)u * ld * (BF16 ? 2 : 4);
+        for (int u0 = t + 4 * wave; u0 < end; u0 += 32) {
+            const int u = u0 + (lane >> 4);
             float p[Q], m = -INFINITY, total = 0.f;
+            load_row<Q, BF16>(logits, (int64_t)min(u, end - 1) * ld, e0, r.E, vec, p);
+            if (r.softmax) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                p[q] = lane + 64 * q < r.E ? load_logit<BF16>(row, lane + 64 * q) : -INFINITY;
-                m = fmaxf(m, p[q]);
+                for (int q = 0; q < Q; ++q) m = fmaxf(m, p[q]);
+                m = row_maxf(m);
             }
-            if (r.softmax) m = wave_max_f32(m, kWave);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                p[q] = r.softmax ? softmax_term(p[q], m) : sigmoid_f32(p[q]);
+                p[q] = r.softmax ? (m == -INFINITY ? 0.f : fast_exp(p[q] - m)) : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
                 total += p[q];
             }
-            total = wave_sum_f32(total);
+            total = row_sum(total);
+            const float c = u < end && total != 0.f ? 1.f / total : 0.f;
 #pragma unroll
-            for (int q = 0; q < Q; ++q) sum[q] += total == 0.f ? 0.f : p[q] / total;
+            for (int q = 0; q < Q; ++q) sum[q] += p[q] * c;
         }
+        // the wave's four rows, then the waves, in a fixed order
 #pragma unroll
-        for (int q = 0; q < Q; ++q) share[wave][lane + 64 * q] = sum[q];
+        for (int q = 0; q < Q; ++q) {
+            sum[q] += __shfl_xor(sum[q], 16, kWave);
+            sum[q] += __shfl_xor(sum[q], 32, kWave);
+            if (lane < 16) share[wave][e0 + q] = sum[q];
+        }
         __syncthreads();
-        for (int i = t * r.k + tid; i < end * r.k; i += 256) {
+        for (int i = t * r.k + tid; i < end * r.k; i += 512) {
             const int e = idx[i];
             if (e >= 0 && e < r.E) atomicAdd(&hist[e], 1);
         }
         __syncthreads();
         const int64_t slot = (int64_t)blockIdx.x + s;
-        for (int e = tid; e < r.E; e += 256) {
-            part[slot * r.E + e] = share[0][e] + share[1][e] + share[2][e] + share[3][e];
+        for (int e = tid; e < r.E; e += 512) {
+            float v = share[0][e];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) v += share[w][e];
+            part[slot * r.E + e] = v;
             count[slot * r.E + e] = hist[e];
         }
         __syncthreads();
@@ -683,46 +758,65 @@ __global__ __launch_bounds__(256) void k_balance_part(SelectRule r, int T, const
     }
 }
 
-// One workgroup per sequence: its slots added in order, load_e = E count_e /
-// (k n), loss = alpha sum_e load_e mean_e.  A sequence without tokens has no
-// loss and no load.
-__global__ __launch_bounds__(256) void k_balance_sum(int E, int k, int T, const int32_t *__restrict__ seq, float alpha,
-                                                     const float *__restrict__ part, const int32_t *__restrict__ count,
-                                                     float *__restrict__ loss, float *__restrict__ load) {
-    __shared__ double wsum[4];
-    const int s = blockIdx.x, tid = threadIdx.x;
+// One workgroup per sequence: its slots added in order (by 1024 / width slices, the
+// slices in order), load_e = E count_e / (k n), loss = alpha sum_e load_e mean_e.
+// A sequence without tokens has no loss and no load.
+template <int WIDTH>
+__global__ __launch_bounds__(1024) void k_balance_sum(int E, int k, int T, const int32_t *__restrict__ seq, float alpha,
+                                                      const float *__restrict__ part, const int32_t *__restrict__ count,
+                                                      float *__restrict__ loss, float *__restrict__ load) {
+    constexpr int kSlices = 1024 / WIDTH;
+    __shared__ double sums[kSlices][WIDTH];
+    __shared__ int32_t counts[kSlices][WIDTH];
+    __shared__ double wsum[16];
+    const int s = blockIdx.x, tid = threadIdx.x, e = tid % WIDTH, slice = tid / WIDTH;
     const int a = min(max(seq[s], 0), T), b = min(max(seq[s + 1], 0), T), n = b - a;
+    double sum = 0.0;
+    int c = 0;
+    if (n > 0 && e < E) {
+        const int64_t first = a / kBalanceTokens + s, last = (b - 1) / kBalanceTokens + s;
+#pragma unroll 8
+        for (int64_t i = first + slice; i <= last; i += kSlices) {
+            sum += part[i * E + e];
+            c += count[i * E + e];
+        }
+    }
+    sums[slice][e] = sum;
+    counts[slice][e] = c;
+    __syncthreads();
     double mine = 0.0;
-    for (int e = tid; e < E; e += 256) {
-        double sum = 0.0;
-        int64_t c = 0;
-        if (n > 0)
-            for (int64_t i = a / kBalanceTokens + s; i <= (int64_t)(b - 1) / kBalanceTokens + s; ++i) {
-                sum += part[i * E + e];
-                c += count[i * E + e];
-            }
+    if (tid < E) {
+#pragma unroll
+        for (int i = 1; i < kSlices; ++i) {
+            sum += sums[i][e];
+            c += counts[i][e];
+        }
         const double f = n > 0 ? (double)E * (double)c / ((double)k * n) : 0.0;
         load[(int64_t)s * E + e] = (float)f;
-        if (n > 0) mine += f * sum / n;
+        if (n > 0) mine = f * sum / n;
     }
     mine = wave_sum_f64(mine);
     if ((tid & 63) == 0) wsum[tid >> 6] = mine;
     __syncthreads();
-    if (tid == 0) loss[s] = (float)((double)alpha * (wsum[0] + wsum[1] + wsum[2] + wsum[3]));
+    if (tid == 0) {
+        double v = 0.0;
+        for (int w = 0; w < 16; ++w) v += wsum[w];
+        loss[s] = (float)((double)alpha * v);
+    }
 }
 
 int balance_blocks(int T) { return (T + kBalanceTokens - 1) / kBalanceTokens; }
 
 }  // namespace
 
-// Experts per lane: the next power of two of E / 64.
-#define MOE_BY_WIDTH(LAUNCH)                       \
-    do {                                           \
-        if (a.rule.E <= 64) LAUNCH(1);             \
-        else if (a.rule.E <= 128) LAUNCH(2);       \
-        else if (a.rule.E <= 256) LAUNCH(4);       \
-        else if (a.rule.E <= 512) LAUNCH(8);       \
-        else LAUNCH(16);                           \
+// LAUNCH(experts per lane): the next power of two of E over LANES.
+#define MOE_BY_WIDTH(LAUNCH, LANES)                      \
+    do {                                                 \
+        if (a.rule.E <= 64) LAUNCH(64 / LANES);          \
+        else if (a.rule.E <= 128) LAUNCH(128 / LANES);   \
+        else if (a.rule.E <= 256) LAUNCH(256 / LANES);   \
+        else if (a.rule.E <= 512) LAUNCH(512 / LANES);   \
+        else LAUNCH(1024 / LANES);                       \
     } while (0)
 
 // Lanes per group of k_select_fast<Q>, 0 where its exchanges do not fit the
@@ -740,9 +834,7 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
     const int lanes = r.E <= 512 ? group_lanes(r, Q) : 0;
     if (lanes) {
         const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16));
-        const int64_t bytes = a.bf16 ? 2 : 4, step = Q * bytes < 16 ? Q * bytes : 16;
-        const bool vec = r.E % Q == 0 && reinterpret_cast<uintptr_t>(a.logits) % step == 0 && a.ld * bytes % step == 0 &&
-                         reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+        const bool vec = rows_vec(Q, r.E, a.bf16, a.logits, a.ld, a.bias);
 #define FAST(QQ)                                                                                                     \
     do {                                                                                                             \
         if (a.bias && a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, true>), grid, block, 0, s, r, lanes,   \
@@ -769,21 +861,22 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
         else hipLaunchKernelGGL((k_select<Q, false>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld, a.bias, a.idx, \
                                 a.weights);                                                                          \
     } while (0)
-    MOE_BY_WIDTH(GO);
+    MOE_BY_WIDTH(GO, 64);
 #undef GO
     return hipGetLastError();
 }
 
 hipError_t launch_select_backward(const SelectBackwardArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)a.T + 3) / 4)), block(256);
-#define GO(Q)                                                                                                     \
-    do {                                                                                                          \
-        if (a.bf16) hipLaunchKernelGGL((k_select_backward<Q, true>), grid, block, 0, s, a.rule, a.T, a.logits,     \
-                                       a.ld, a.idx, a.dweights, a.balance, a.dlogits);                            \
-        else hipLaunchKernelGGL((k_select_backward<Q, false>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld,    \
-                                a.idx, a.dweights, a.balance, a.dlogits);                                         \
+    const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16)), block(256);
+#define GO(Q)                                                                                                          \
+    do {                                                                                                               \
+        const bool vec = rows_vec(Q, a.rule.E, a.bf16, a.logits, a.ld, a.dlogits, a.balance.load);                     \
+        if (a.bf16) hipLaunchKernelGGL((k_select_backward<Q, true>), grid, block, 0, s, a.rule, vec, a.T, a.logits,    \
+                                       a.ld, a.idx, a.dweights, a.balance, a.dlogits);                                 \
+        else hipLaunchKernelGGL((k_select_backward<Q, false>), grid, block, 0, s, a.rule, vec, a.T, a.logits, a.ld,    \
+                                a.idx, a.dweights, a.balance, a.dlogits);                                              \
     } while (0)
-    MOE_BY_WIDTH(GO);
+    MOE_BY_WIDTH(GO, 16);
 #undef GO
     return hipGetLastError();
 }
@@ -796,20 +889,24 @@ hipError_t launch_balance_loss(const BalanceArgs &a, void *ws, hipStream_t s) {
     const size_t slots = (size_t)balance_blocks(a.T) + a.n_seq;
     float *part = static_cast<float *>(ws);
     int32_t *count = reinterpret_cast<int32_t *>(part + slots * a.rule.E);
-    const dim3 grid(balance_blocks(a.T)), block(256);
-#define GO(Q)                                                                                                       \
-    do {                                                                                                            \
-        if (a.bf16) hipLaunchKernelGGL((k_balance_part<Q, true>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld,   \
-                                       a.idx, a.seq, a.n_seq, part, count);                                         \
-        else hipLaunchKernelGGL((k_balance_part<Q, false>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld, a.idx,  \
-                                a.seq, a.n_seq, part, count);                                                       \
+    const dim3 grid(balance_blocks(a.T)), block(512);
+#define GO(Q)                                                                                                         \
+    do {                                                                                                              \
+        const bool vec = rows_vec(Q, a.rule.E, a.bf16, a.logits, a.ld, nullptr);                                      \
+        if (a.bf16) hipLaunchKernelGGL((k_balance_part<Q, true>), grid, block, 0, s, a.rule, vec, a.T, a.logits,      \
+                                       a.ld, a.idx, a.seq, a.n_seq, part, count);                                     \
+        else hipLaunchKernelGGL((k_balance_part<Q, false>), grid, block, 0, s, a.rule, vec, a.T, a.logits, a.ld,      \
+                                a.idx, a.seq, a.n_seq, part, count);                                                  \
     } while (0)
-    MOE_BY_WIDTH(GO);
+    MOE_BY_WIDTH(GO, 16);
 #undef GO
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_balance_sum, dim3(a.n_seq), block, 0, s, a.rule.E, a.rule.k, a.T, a.seq, a.alpha, part, count,
-                       a.loss, a.load);
+#define GO(W)                                                                                                         \
+    hipLaunchKernelGGL(k_balance_sum<W>, dim3(a.n_seq), dim3(1024), 0, s, a.rule.E, a.rule.k, a.T, a.seq, a.alpha,    \
+                       part, count, a.loss, a.load)
+    MOE_BY_WIDTH(GO, 1);
+#undef GO
     return hipGetLastError();
 }
 #undef MOE_BY_WIDTH
