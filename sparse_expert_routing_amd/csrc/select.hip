@@ -571,15 +571,28 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
     const bool dense = b.seq || (r.softmax && !r.renorm);
     float p[Q], m = -INFINITY, total = 0.f;
     float *const row_acc = &acc[wave][(lane & 48) * Q];
+    // what the places of idx say, asked for ahead of all else
+    const int places = dw ? (r.k + 15) / 16 : 0;
+    float d[4], le[4];
+    int e[4];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) acc[wave][lane * Q + q] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        if (i >= places) continue;
+        const int j = 16 * i + sub;
+        e[i] = j < r.k ? idx[t * r.k + j] : -1;
+        d[i] = j < r.k ? dw[t * r.k + j] : 0.f;
+    }
     if (dense) {
         load_row<Q, BF16>(logits, t * ld, e0, r.E, vec, p);
-        if (r.softmax) {
+    }
 #pragma unroll
-            for (int q = 0; q < Q; ++q) m = fmaxf(m, p[q]);
-            m = row_maxf(m);
-        }
+    for (int i = 0; i < 4; ++i) {
+        if (i >= places) continue;
+        const bool on = e[i] >= 0 && e[i] < r.E;
+        if (!on) e[i] = -1;
+        le[i] = load_logit<BF16>(static_cast<const char *>(logits) + t * ld * (BF16 ? 2 : 4), on ? e[i] : 0);
+        le[i] = on ? le[i] : -INFINITY;
+        d[i] = on ? r.scale * d[i] : 0.f;
     }
     // the balance loss's coefficients of the row's sequence
     float f[Q], scale = 0.f;
@@ -598,8 +611,15 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
         load_f32<Q>(b.load, (int64_t)at * r.E, e0, r.E, vec, f);
     }
     float mean = 0.f;  // softmax weights as they are: sum_j c dw_j p_j
+#pragma unroll
+    for (int q = 0; q < Q; ++q) acc[wave][lane * Q + q] = 0.f;
     wave_sync();
     if (dense) {
+        if (r.softmax) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) m = fmaxf(m, p[q]);
+            m = row_maxf(m);
+        }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             // (a sigmoid's p keeps the logit until its share is known)
@@ -611,21 +631,10 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
         total = row_sum(total);
     }
     if (dw) {
-        float d[4], share[4], le[4];
-        int e[4];
-        float mc = -INFINITY, S = 0.f, cross = 0.f;
-        const int places = (r.k + 15) / 16;
+        float share[4], mc = -INFINITY, S = 0.f, cross = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i >= places) continue;
-            const int j = 16 * i + sub;
-            e[i] = j < r.k ? idx[t * r.k + j] : -1;
-            const bool on = e[i] >= 0 && e[i] < r.E;
-            if (!on) e[i] = -1;
-            le[i] = on ? load_logit<BF16>(static_cast<const char *>(logits) + t * ld * (BF16 ? 2 : 4), e[i]) : -INFINITY;
-            d[i] = on ? r.scale * dw[t * r.k + j] : 0.f;
-            mc = fmaxf(mc, le[i]);
-        }
+        for (int i = 0; i < 4; ++i)
+            if (i < places) mc = fmaxf(mc, le[i]);
         if (r.softmax) mc = r.renorm ? row_maxf(mc) : m;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -659,7 +668,9 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
         if (b.seq) {
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                f[q] = e0 + q < r.E ? scale * f[q] : 0.f;
+                // from the mean load, 1: the shares' sum is 1, so a constant has no gradient, and
+                // what is left rounds by its own size
+                f[q] = e0 + q < r.E ? scale * (f[q] - 1.f) : 0.f;
                 const float v = r.softmax ? p[q] : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
                 dot += f[q] * (v * inv);
             }
