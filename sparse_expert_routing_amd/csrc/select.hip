@@ -328,12 +328,53 @@ __device__ __forceinline__ void load_f32(const float *p, int64_t at, int e0, int
     load_row<Q, false>(p, at, e0, E, vec, v);
 }
 
+// Four experts per lane and load, 64 experts on for the next: the expert of a
+// lane's value q.  Sixteen lanes then read and write a row in order.
+__device__ __forceinline__ int spread(int sub, int q) { return (q >> 2) * 64 + 4 * sub + (q & 3); }
+
+// A row's experts spread over its sixteen lanes, `behind` behind the last one.
+// vec: rows begin at four values, E is a multiple of four.
+template <int Q, bool BF16>
+__device__ __forceinline__ void load_spread(const void *p, int64_t at, int sub, int E, bool vec, float behind,
+                                            float (&l)[Q]) {
+    const char *row = static_cast<const char *>(p) + at * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int c = 0; c < Q; c += 4) {
+        const int e = spread(sub, c);
+        if (vec) {
+            const int from = e < E ? e : 0;
+            if (BF16) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(row + 2 * from);
+                l[c] = bf16_to_f32(v.x & 0xffffu);
+                l[c + 1] = bf16_to_f32(v.x >> 16);
+                l[c + 2] = bf16_to_f32(v.y & 0xffffu);
+                l[c + 3] = bf16_to_f32(v.y >> 16);
+            } else {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(row + 4 * from);
+                l[c] = v[0]; l[c + 1] = v[1]; l[c + 2] = v[2]; l[c + 3] = v[3];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[c + i] = load_logit<BF16>(row, min(e + i, E - 1));
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) l[q] = spread(sub, q) < E ? l[q] : behind;
+}
+// Whether load_spread can load whole vectors of rows ld apart, and of dense fp32
+// rows beside them.
+bool spread_vec(int E, bool bf16, const void *logits, int64_t ld, const void *a, const void *b) {
+    const int64_t bytes = bf16 ? 8 : 16;
+    return E % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % bytes == 0 && ld % 4 == 0 &&
+           reinterpret_cast<uintptr_t>(a) % 16 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0;
+}
+
 // Whether load_row can load whole vectors of rows ld apart, and of a dense fp32
-// array beside them.
-bool rows_vec(int Q, int E, bool bf16, const void *logits, int64_t ld, const void *a, const void *b = nullptr) {
+// row beside them.
+bool rows_vec(int Q, int E, bool bf16, const void *logits, int64_t ld, const void *a) {
     const int64_t bytes = bf16 ? 2 : 4, step = Q * bytes < 16 ? Q * bytes : 16;
     return E % Q == 0 && reinterpret_cast<uintptr_t>(logits) % step == 0 && ld * bytes % step == 0 &&
-           reinterpret_cast<uintptr_t>(a) % 16 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0;
+           reinterpret_cast<uintptr_t>(a) % 16 == 0;
 }
 
 // What the keys are made of: bf16 logits with the id in the low bits (no two
@@ -567,10 +608,9 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
     if (t0 >= T) return;
     const int64_t t = min(t0 + (lane >> 4), (int64_t)T - 1);
     const bool mine = t0 + (lane >> 4) < T;
-    const int e0 = sub * Q;
     const bool dense = b.seq || (r.softmax && !r.renorm);
-    float p[Q], m = -INFINITY, total = 0.f;
-    float *const row_acc = &acc[wave][(lane & 48) * Q];
+    float p[Q], x[Q], m = -INFINITY, total = 0.f;
+    float *const row_acc = &acc[wave][(lane & 48) * Q];  // by expert
     // what the places of idx say, asked for ahead of all else
     const int places = dw ? (r.k + 15) / 16 : 0;
     float d[4], le[4];
@@ -583,7 +623,7 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
         d[i] = j < r.k ? dw[t * r.k + j] : 0.f;
     }
     if (dense) {
-        load_row<Q, BF16>(logits, t * ld, e0, r.E, vec, p);
+        load_spread<Q, BF16>(logits, t * ld, sub, r.E, vec, -INFINITY, p);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -608,11 +648,11 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
         }
         const int at = min(s, b.n_seq - 1), start = b.seq[at], end = b.seq[at + 1];
         if (s < b.n_seq && t >= start && t < end) scale = b.alpha * b.dloss[at] / (float)(end - start);
-        load_f32<Q>(b.load, (int64_t)at * r.E, e0, r.E, vec, f);
+        load_spread<Q, false>(b.load, (int64_t)at * r.E, sub, r.E, vec, 1.f, f);
     }
     float mean = 0.f;  // softmax weights as they are: sum_j c dw_j p_j
 #pragma unroll
-    for (int q = 0; q < Q; ++q) acc[wave][lane * Q + q] = 0.f;
+    for (int q = 0; q < Q; ++q) row_acc[spread(sub, q)] = 0.f;
     wave_sync();
     if (dense) {
         if (r.softmax) {
@@ -622,11 +662,14 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            // (a sigmoid's p keeps the logit until its share is known)
-            const float v = r.softmax ? (m == -INFINITY ? 0.f : fast_exp(p[q] - m))
-                                      : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
-            total += v;
-            if (r.softmax) p[q] = v;
+            // p becomes the score, x what gives a sigmoid's 1 - p = x p
+            if (r.softmax) {
+                p[q] = m == -INFINITY ? 0.f : fast_exp(p[q] - m);
+            } else {
+                x[q] = fast_exp(-p[q]);
+                p[q] = __builtin_amdgcn_rcpf(1.0f + x[q]);
+            }
+            total += p[q];
         }
         total = row_sum(total);
     }
@@ -661,7 +704,7 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
     wave_sync();
     float g[Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) g[q] = acc[wave][lane * Q + q];
+    for (int q = 0; q < Q; ++q) g[q] = row_acc[spread(sub, q)];
     if (dense) {
         const float inv = total == 0.f ? 0.f : 1.f / total;
         float dot = 0.f;
@@ -670,34 +713,29 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
             for (int q = 0; q < Q; ++q) {
                 // from the mean load, 1: the shares' sum is 1, so a constant has no gradient, and
                 // what is left rounds by its own size
-                f[q] = e0 + q < r.E ? scale * (f[q] - 1.f) : 0.f;
-                const float v = r.softmax ? p[q] : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
-                dot += f[q] * (v * inv);
+                f[q] = scale * (f[q] - 1.f);
+                dot += f[q] * (p[q] * inv);
             }
             dot = row_sum(dot);
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            float v = p[q], rest = 1.f;
-            if (!r.softmax) {
-                const float x = fast_exp(-p[q]);
-                v = __builtin_amdgcn_rcpf(1.0f + x);
-                rest = x > 1e30f ? 1.f : x * v;  // 1 - v
-            }
-            g[q] += v * inv * ((b.seq ? f[q] - dot : 0.f) * rest - mean);
+            const float rest = r.softmax || x[q] > 1e30f ? 1.f : x[q] * p[q];
+            g[q] += p[q] * inv * ((b.seq ? f[q] - dot : 0.f) * rest - mean);
         }
     }
     if (!mine) return;
-    float *o = dlogits + t * r.E + e0;
-    if (vec) {
-        if (e0 < r.E) {
+    float *o = dlogits + t * r.E;
 #pragma unroll
-            for (int q = 0; q < Q; q += 4) *reinterpret_cast<f32x4 *>(o + q) = f32x4{g[q], g[q + 1], g[q + 2], g[q + 3]};
+    for (int c = 0; c < Q; c += 4) {
+        const int e = spread(sub, c);
+        if (vec) {
+            if (e < r.E) *reinterpret_cast<f32x4 *>(o + e) = f32x4{g[c], g[c + 1], g[c + 2], g[c + 3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e + i < r.E) o[e + i] = g[c + i];
         }
-    } else {
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (e0 + q < r.E) o[q] = g[q];
     }
 }
 
@@ -713,7 +751,7 @@ __global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, in
                                                       float *__restrict__ part, int32_t *__restrict__ count) {
     __shared__ float share[8][16 * Q];
     __shared__ int32_t hist[16 * Q];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, e0 = (lane & 15) * Q;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane & 15;
     const int t1 = (int)min((int64_t)(blockIdx.x + 1) * kBalanceTokens, (int64_t)T);
     int t = max((int)((int64_t)blockIdx.x * kBalanceTokens), seq[0]);
     while (t < t1) {
@@ -727,7 +765,7 @@ __global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, in
         for (int u0 = t + 4 * wave; u0 < end; u0 += 32) {
             const int u = u0 + (lane >> 4);
             float p[Q], m = -INFINITY, total = 0.f;
-            load_row<Q, BF16>(logits, (int64_t)min(u, end - 1) * ld, e0, r.E, vec, p);
+            load_spread<Q, BF16>(logits, (int64_t)min(u, end - 1) * ld, sub, r.E, vec, -INFINITY, p);
             if (r.softmax) {
 #pragma unroll
                 for (int q = 0; q < Q; ++q) m = fmaxf(m, p[q]);
@@ -748,7 +786,7 @@ __global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, in
         for (int q = 0; q < Q; ++q) {
             sum[q] += __shfl_xor(sum[q], 16, kWave);
             sum[q] += __shfl_xor(sum[q], 32, kWave);
-            if (lane < 16) share[wave][e0 + q] = sum[q];
+            if (lane < 16) share[wave][spread(sub, q)] = sum[q];
         }
         __syncthreads();
         for (int i = t * r.k + tid; i < end * r.k; i += 512) {
@@ -881,7 +919,7 @@ hipError_t launch_select_backward(const SelectBackwardArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16)), block(256);
 #define GO(Q)                                                                                                          \
     do {                                                                                                               \
-        const bool vec = rows_vec(Q, a.rule.E, a.bf16, a.logits, a.ld, a.dlogits, a.balance.load);                     \
+        const bool vec = spread_vec(a.rule.E, a.bf16, a.logits, a.ld, a.dlogits, a.balance.load);                      \
         if (a.bf16) hipLaunchKernelGGL((k_select_backward<Q, true>), grid, block, 0, s, a.rule, vec, a.T, a.logits,    \
                                        a.ld, a.idx, a.dweights, a.balance, a.dlogits);                                 \
         else hipLaunchKernelGGL((k_select_backward<Q, false>), grid, block, 0, s, a.rule, vec, a.T, a.logits, a.ld,    \
@@ -903,7 +941,7 @@ hipError_t launch_balance_loss(const BalanceArgs &a, void *ws, hipStream_t s) {
     const dim3 grid(balance_blocks(a.T)), block(512);
 #define GO(Q)                                                                                                         \
     do {                                                                                                              \
-        const bool vec = rows_vec(Q, a.rule.E, a.bf16, a.logits, a.ld, nullptr);                                      \
+        const bool vec = spread_vec(a.rule.E, a.bf16, a.logits, a.ld, nullptr, nullptr);                              \
         if (a.bf16) hipLaunchKernelGGL((k_balance_part<Q, true>), grid, block, 0, s, a.rule, vec, a.T, a.logits,      \
                                        a.ld, a.idx, a.seq, a.n_seq, part, count);                                     \
         else hipLaunchKernelGGL((k_balance_part<Q, false>), grid, block, 0, s, a.rule, vec, a.T, a.logits, a.ld,      \
