@@ -231,7 +231,7 @@ struct SelectBackwardArgs {
     float *dlogits;
 };
 hipError_t launch_select_backward(const SelectBackwardArgs &a, hipStream_t s);
-constexpr int kBalanceTokens = 128;  // tokens per workgroup of the loss's partial sums
+constexpr int kBalanceTokens = 64;  // tokens per workgroup of the loss's partial sums
 struct BalanceArgs {
     SelectRule rule;  // E, k and softmax are read
     int T;
