@@ -174,64 +174,99 @@ __device__ __forceinline__ void put8(void *base, int64_t at, const float (&v)[8]
     store8<!F32, true>(base, at, 8, v);
 }
 
-// Eight consecutive saved values of row r at column c.
+// Eight consecutive saved values of row r at column c: as they lie in memory, so
+// that several rows' loads are in flight, and then their values.
 template <int FMT>
-__device__ __forceinline__ void saved8(const Saved &y, int64_t r, int d, int ntile, int c, float (&v)[8]) {
-    if (FMT == kCkptBF16) {
-        load8<true, true>(y.data, r * d + c, 8, v);
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(y.data) + r * d + c);
-        const float scale = pow2_of_byte(y.scales[r * ntile + c / kTile]);
-        float lo[4], hi[4];
-        decode4<FMT>(w.x, lo);
-        decode4<FMT>(w.y, hi);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { v[i] = lo[i] * scale; v[4 + i] = hi[i] * scale; }
+struct Saved8 {
+    i32x4 w;  // bf16: all four words; 8-bit: the first two
+    uint32_t byte;
+    __device__ __forceinline__ void load(const Saved &y, int64_t r, int d, int ntile, int c) {
+        if (FMT == kCkptBF16) {
+            w = *reinterpret_cast<const i32x4 *>(static_cast<const uint16_t *>(y.data) + r * d + c);
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(y.data) + r * d + c);
+            w = i32x4{(int)v.x, (int)v.y, 0, 0};
+            byte = y.scales[r * ntile + c / kTile];
+        }
     }
-}
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        if (FMT == kCkptBF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf16_to_f32((uint32_t)w[i] & 0xffffu);
+                v[2 * i + 1] = bf16_to_f32((uint32_t)w[i] >> 16);
+            }
+        } else {
+            const float scale = pow2_of_byte(byte);
+            float lo[4], hi[4];
+            decode4<FMT>((uint32_t)w[0], lo);
+            decode4<FMT>((uint32_t)w[1], hi);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { v[i] = lo[i] * scale; v[4 + i] = hi[i] * scale; }
+        }
+    }
+};
 
-// One wave per token.  A row_of entry outside [0, T*8) is a choice that was not
-// dispatched: it has no row to write and its gradient is 0.
-template <int FMT, bool F32>
+// W waves per token, each on every W-th run of 512 columns.  A row_of entry outside
+// [0, T*8) is a choice that was not dispatched: it has no row to write and its
+// gradient is 0.
+template <int FMT, bool F32, int W>
 __global__ __launch_bounds__(256) void k_combine_backward(int T, int d, int ntile, const float *__restrict__ dy, Saved y,
                                                           const int32_t *__restrict__ row_of, const float *__restrict__ w,
                                                           void *__restrict__ dyp, void *__restrict__ dys,
                                                           float *__restrict__ dg) {
+    __shared__ float part[4][8];
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= T) return;
-    int r[8];
-    float g[8], dot[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        r[j] = row_of[t * 8 + j];
-        if (r[j] < 0 || (int64_t)r[j] >= (int64_t)T * 8) r[j] = -1;
-        g[j] = w[t * 8 + j];
-        dot[j] = 0.f;
-    }
-    for (int c = 8 * lane; c < d; c += 512) {
-        float v[8];
-        load8<false, true>(dy, t * d + c, 8, v);
-        if (dys) put8<F32>(dys, t * d + c, v);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * (4 / W) + wave / W;
+    float mine = 0.f;
+    if (t < T) {
+        int r[8];
+        float g[8], dot[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if (r[j] < 0) continue;
-            float s[8], o[8];
-            saved8<FMT>(y, r[j], d, ntile, c, s);
+            r[j] = row_of[t * 8 + j];
+            if (r[j] < 0 || (int64_t)r[j] >= (int64_t)T * 8) r[j] = -1;
+            g[j] = w[t * 8 + j];
+            dot[j] = 0.f;
+        }
+        for (int c = 8 * lane + 512 * (wave % W); c < d; c += 512 * W) {
+            float v[8];
+            Saved8<FMT> in[8];
+            load8<false, true>(dy, t * d + c, 8, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dot[j] += v[i] * s[i];
-                o[i] = g[j] * v[i];
+            for (int j = 0; j < 8; ++j) in[j].load(y, max(r[j], 0), d, ntile, c);
+            if (dys) put8<F32>(dys, t * d + c, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float s[8], o[8];
+                in[j].values(s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot[j] += v[i] * s[i];
+                    o[i] = g[j] * v[i];
+                }
+                if (r[j] >= 0) put8<F32>(dyp, (int64_t)r[j] * d + c, o);
             }
-            put8<F32>(dyp, (int64_t)r[j] * d + c, o);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float v = dot[j];
+#pragma unroll
+            for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
+            if (lane == j) mine = r[j] >= 0 ? v : 0.f;
         }
     }
+    if (W == 1) {
+        if (t < T && lane < 8) dg[t * 8 + lane] = mine;
+        return;
+    }
+    if (lane < 8) part[wave][lane] = mine;
+    __syncthreads();
+    if (t < T && wave % W == 0 && lane < 8) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float v = dot[j];
-#pragma unroll
-        for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, kWave);
-        if (lane == j) dg[t * 8 + j] = v;
+        for (int i = 1; i < W; ++i) mine += part[wave + i][lane];
+        dg[t * 8 + lane] = mine;
     }
 }
 
@@ -283,19 +318,26 @@ hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s) {
 
 hipError_t launch_combine_backward(int T, int d, const float *dy, const Saved &y, const int32_t *row_of,
                                    const float *weights, void *dyp, void *dys, float *dg, bool f32_out, hipStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)T + 3) / 4)), block(256);
     const int ntile = (d + kTile - 1) / kTile;
-#define GO(FMT)                                                                                                   \
-    do {                                                                                                          \
-        if (f32_out) hipLaunchKernelGGL((k_combine_backward<FMT, true>), grid, block, 0, s, T, d, ntile, dy, y,   \
-                                        row_of, weights, dyp, dys, dg);                                           \
-        else hipLaunchKernelGGL((k_combine_backward<FMT, false>), grid, block, 0, s, T, d, ntile, dy, y, row_of,  \
-                                weights, dyp, dys, dg);                                                           \
+    const dim3 block(256);
+#define GO_W(FMT, W)                                                                                               \
+    do {                                                                                                           \
+        const dim3 grid((unsigned)(((int64_t)T * W + 3) / 4));                                                     \
+        if (f32_out) hipLaunchKernelGGL((k_combine_backward<FMT, true, W>), grid, block, 0, s, T, d, ntile, dy, y, \
+                                        row_of, weights, dyp, dys, dg);                                            \
+        else hipLaunchKernelGGL((k_combine_backward<FMT, false, W>), grid, block, 0, s, T, d, ntile, dy, y,        \
+                                row_of, weights, dyp, dys, dg);                                                    \
+    } while (0)
+#define GO(FMT)                     \
+    do {                            \
+        if (d >= 2048) GO_W(FMT, 4); \
+        else GO_W(FMT, 1);          \
     } while (0)
     if (y.format == kCkptE4M3) GO(kCkptE4M3);
     else if (y.format == kCkptI8) GO(kCkptI8);
     else GO(kCkptBF16);
 #undef GO
+#undef GO_W
     return hipGetLastError();
 }
 
