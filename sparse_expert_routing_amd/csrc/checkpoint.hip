@@ -89,10 +89,10 @@ __device__ __forceinline__ void store8(void *dst, int64_t at, int n, const float
         i32x4 w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = (int)pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(dst) + at) = w;
+        __builtin_nontemporal_store(w, reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(dst) + at));
     } else if (VEC) {
-        *reinterpret_cast<f32x4 *>(static_cast<float *>(dst) + at) = f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4 *>(static_cast<float *>(dst) + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4 *>(static_cast<float *>(dst) + at));
+        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4 *>(static_cast<float *>(dst) + at + 4));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
