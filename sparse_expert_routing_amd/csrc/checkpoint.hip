@@ -103,67 +103,120 @@ __device__ __forceinline__ void store8(void *dst, int64_t at, int n, const float
     }
 }
 
-// Sixteen lanes per tile, eight values each.
-template <bool BF16, int FMT, bool VEC>
+// A tile's place: row and column of its first value.  FLAT: rows are dense and
+// hold whole tiles, so a tile is 128 values in a row of the whole array; else one
+// division per tile by the tiles of a row, from the row of the workgroup's first.
+struct TilePlace {
+    int64_t row;
+    int first;  // tile of the row that the workgroup begins with
+};
+template <bool FLAT>
+__device__ __forceinline__ TilePlace place_of(int64_t base, int ntile) {
+    if (FLAT) return TilePlace{0, 0};
+    const int64_t row = base / ntile;
+    return TilePlace{row, (int)(base - row * ntile)};
+}
+
+// Sixteen lanes per tile, eight values each; kUnroll tiles of a lane in flight.
+constexpr int kUnroll = 4;
+template <bool BF16, int FMT, bool VEC, bool FLAT>
 __global__ __launch_bounds__(256) void k_pack(int64_t rows, int cols, int ntile, const void *__restrict__ src, int64_t ld,
                                               uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
-    const int sub = threadIdx.x & 15;
-    const int64_t tiles = rows * ntile, step = (int64_t)gridDim.x * 16;
-    for (int64_t base = (int64_t)blockIdx.x * 16; base < tiles; base += step) {
-        const int64_t tile = base + (threadIdx.x >> 4);
-        const bool on = tile < tiles;
-        const int64_t row = on ? tile / ntile : 0;
-        const int c = (int)(on ? tile - row * ntile : 0) * kTile + sub * 8;
-        const int n = on ? min(8, cols - c) : 0;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (n > 0) load8<BF16, VEC>(src, row * ld + c, n, v);
-        uint32_t m = 0;
+    const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
+    const int64_t tiles = rows * ntile, step = (int64_t)gridDim.x * (16 * kUnroll);
+    for (int64_t base = (int64_t)blockIdx.x * (16 * kUnroll); base < tiles; base += step) {
+        const TilePlace at = place_of<FLAT>(base, ntile);
+        float v[kUnroll][8];
+        int64_t from[kUnroll];  // where the lane's values lie in codes
+        int n[kUnroll];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-        for (int s = 8; s >= 1; s >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, s, kWave));
-        const uint32_t byte = tile_byte<FMT>(m);
-        if (!on) continue;
-        if (sub == 0) scales[tile] = (uint8_t)byte;
-        if (n <= 0) continue;
-        const float inv = byte == 255u ? 0.f : inverse_pow2(byte);
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t tile = base + 16 * u + group;
+            int64_t row = 0;
+            int c = sub * 8;
+            if (!FLAT) {
+                const uint32_t k = (uint32_t)(at.first + 16 * u + group), q = k / (uint32_t)ntile;
+                row = at.row + q;
+                c += (int)(k - q * ntile) * kTile;
+            }
+            n[u] = tile < tiles ? (FLAT ? 8 : min(8, cols - c)) : 0;
+            from[u] = FLAT ? tile * kTile + c : row * cols + c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = byte == 255u ? 0.f : v[i] * inv;
-        const uint2 w = uint2{encode4<FMT>(v[0], v[1], v[2], v[3]), encode4<FMT>(v[4], v[5], v[6], v[7])};
-        if (VEC) {
-            *reinterpret_cast<uint2 *>(codes + row * cols + c) = w;
-        } else {
+            for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+            if (n[u] > 0) load8<BF16, VEC>(src, FLAT ? from[u] : row * ld + c, n[u], v[u]);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) codes[row * cols + c + i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+        for (int u = 0; u < kUnroll; ++u) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[u][i]) & 0x7fffffffu);
+            const uint32_t byte = tile_byte<FMT>(row_max(m));
+            if (base + 16 * u + group >= tiles) continue;
+            if (sub == 0) scales[base + 16 * u + group] = (uint8_t)byte;
+            if (n[u] <= 0) continue;
+            const float inv = inverse_pow2(byte);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = byte == 255u ? 0.f : v[u][i] * inv;
+            const uint2 w = uint2{encode4<FMT>(v[u][0], v[u][1], v[u][2], v[u][3]),
+                                  encode4<FMT>(v[u][4], v[u][5], v[u][6], v[u][7])};
+            if (VEC) {
+                *reinterpret_cast<uint2 *>(codes + from[u]) = w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n[u]) codes[from[u] + i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+            }
         }
     }
 }
 
-template <bool BF16, int FMT, bool VEC>
+template <bool BF16, int FMT, bool VEC, bool FLAT>
 __global__ __launch_bounds__(256) void k_unpack(int64_t rows, int cols, int ntile, const uint8_t *__restrict__ codes,
                                                 const uint8_t *__restrict__ scales, void *__restrict__ dst, int64_t ld) {
-    const int sub = threadIdx.x & 15;
-    const int64_t tiles = rows * ntile, step = (int64_t)gridDim.x * 16;
-    for (int64_t tile = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); tile < tiles; tile += step) {
-        const int64_t row = tile / ntile;
-        const int c = (int)(tile - row * ntile) * kTile + sub * 8;
-        const int n = min(8, cols - c);
-        if (n <= 0) continue;
-        const float scale = pow2_of_byte(scales[tile]);
-        uint2 w = uint2{0u, 0u};
-        if (VEC) {
-            w = *reinterpret_cast<const uint2 *>(codes + row * cols + c);
-        } else {
+    const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
+    const int64_t tiles = rows * ntile, step = (int64_t)gridDim.x * (16 * kUnroll);
+    for (int64_t base = (int64_t)blockIdx.x * (16 * kUnroll); base < tiles; base += step) {
+        const TilePlace at = place_of<FLAT>(base, ntile);
+        uint2 w[kUnroll];
+        uint32_t byte[kUnroll];
+        int64_t to[kUnroll];
+        int n[kUnroll];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) (i < 4 ? w.x : w.y) |= (uint32_t)codes[row * cols + c + i] << (8 * (i & 3));
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t tile = base + 16 * u + group;
+            int64_t row = 0;
+            int c = sub * 8;
+            if (!FLAT) {
+                const uint32_t k = (uint32_t)(at.first + 16 * u + group), q = k / (uint32_t)ntile;
+                row = at.row + q;
+                c += (int)(k - q * ntile) * kTile;
+            }
+            n[u] = tile < tiles ? (FLAT ? 8 : min(8, cols - c)) : 0;
+            const int64_t from = FLAT ? tile * kTile + c : row * cols + c;
+            to[u] = FLAT ? from : row * ld + c;
+            w[u] = uint2{0u, 0u};
+            byte[u] = 127u;
+            if (n[u] <= 0) continue;
+            byte[u] = scales[tile];
+            if (VEC) {
+                w[u] = *reinterpret_cast<const uint2 *>(codes + from);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n[u]) (i < 4 ? w[u].x : w[u].y) |= (uint32_t)codes[from + i] << (8 * (i & 3));
+            }
         }
-        float lo[4], hi[4], v[8];
-        decode4<FMT>(w.x, lo);
-        decode4<FMT>(w.y, hi);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { v[i] = lo[i] * scale; v[4 + i] = hi[i] * scale; }
-        store8<BF16, VEC>(dst, row * ld + c, n, v);
+        for (int u = 0; u < kUnroll; ++u) {
+            if (n[u] <= 0) continue;
+            const float scale = pow2_of_byte(byte[u]);
+            float lo[4], hi[4], v[8];
+            decode4<FMT>(w[u].x, lo);
+            decode4<FMT>(w[u].y, hi);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { v[i] = lo[i] * scale; v[4 + i] = hi[i] * scale; }
+            store8<BF16, VEC>(dst, to[u], n[u], v);
+        }
     }
 }
 
@@ -278,30 +331,30 @@ bool vec_ok(const CkptArgs &a, const void *plain) {
 }
 
 unsigned tile_grid(int64_t tiles) {
-    const int64_t n = (tiles + 15) / 16;
+    const int64_t n = (tiles + 16 * kUnroll - 1) / (16 * kUnroll);
     return (unsigned)(n < (1 << 22) ? n : (1 << 22));
 }
 
 }  // namespace
 
+#define MOE_CKPT_TYPES(KERNEL, FMT, ...)                                                                  \
+    do {                                                                                                  \
+        if (a.bf16 && flat) hipLaunchKernelGGL((KERNEL<true, FMT, true, true>), __VA_ARGS__);             \
+        else if (a.bf16 && vec) hipLaunchKernelGGL((KERNEL<true, FMT, true, false>), __VA_ARGS__);        \
+        else if (a.bf16) hipLaunchKernelGGL((KERNEL<true, FMT, false, false>), __VA_ARGS__);              \
+        else if (flat) hipLaunchKernelGGL((KERNEL<false, FMT, true, true>), __VA_ARGS__);                 \
+        else if (vec) hipLaunchKernelGGL((KERNEL<false, FMT, true, false>), __VA_ARGS__);                 \
+        else hipLaunchKernelGGL((KERNEL<false, FMT, false, false>), __VA_ARGS__);                         \
+    } while (0)
 #define MOE_CKPT_VARIANTS(KERNEL, ...)                                                                    \
     do {                                                                                                  \
-        if (a.format == kCkptE4M3) {                                                                      \
-            if (a.bf16 && vec) hipLaunchKernelGGL((KERNEL<true, kCkptE4M3, true>), __VA_ARGS__);          \
-            else if (a.bf16) hipLaunchKernelGGL((KERNEL<true, kCkptE4M3, false>), __VA_ARGS__);           \
-            else if (vec) hipLaunchKernelGGL((KERNEL<false, kCkptE4M3, true>), __VA_ARGS__);              \
-            else hipLaunchKernelGGL((KERNEL<false, kCkptE4M3, false>), __VA_ARGS__);                      \
-        } else {                                                                                          \
-            if (a.bf16 && vec) hipLaunchKernelGGL((KERNEL<true, kCkptI8, true>), __VA_ARGS__);            \
-            else if (a.bf16) hipLaunchKernelGGL((KERNEL<true, kCkptI8, false>), __VA_ARGS__);             \
-            else if (vec) hipLaunchKernelGGL((KERNEL<false, kCkptI8, true>), __VA_ARGS__);                \
-            else hipLaunchKernelGGL((KERNEL<false, kCkptI8, false>), __VA_ARGS__);                        \
-        }                                                                                                 \
+        if (a.format == kCkptE4M3) MOE_CKPT_TYPES(KERNEL, kCkptE4M3, __VA_ARGS__);                        \
+        else MOE_CKPT_TYPES(KERNEL, kCkptI8, __VA_ARGS__);                                                \
     } while (0)
 
 hipError_t launch_checkpoint_pack(const CkptArgs &a, hipStream_t s) {
     const int ntile = (a.cols + kTile - 1) / kTile;
-    const bool vec = vec_ok(a, a.src);
+    const bool vec = vec_ok(a, a.src), flat = vec && a.cols % kTile == 0 && a.ld == a.cols;
     const dim3 grid(tile_grid(a.rows * ntile)), block(256);
     MOE_CKPT_VARIANTS(k_pack, grid, block, 0, s, a.rows, a.cols, ntile, a.src, a.ld, a.codes, a.scales);
     return hipGetLastError();
@@ -309,12 +362,13 @@ hipError_t launch_checkpoint_pack(const CkptArgs &a, hipStream_t s) {
 
 hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s) {
     const int ntile = (a.cols + kTile - 1) / kTile;
-    const bool vec = vec_ok(a, a.dst);
+    const bool vec = vec_ok(a, a.dst), flat = vec && a.cols % kTile == 0 && a.ld == a.cols;
     const dim3 grid(tile_grid(a.rows * ntile)), block(256);
     MOE_CKPT_VARIANTS(k_unpack, grid, block, 0, s, a.rows, a.cols, ntile, a.codes, a.scales, a.dst, a.ld);
     return hipGetLastError();
 }
 #undef MOE_CKPT_VARIANTS
+#undef MOE_CKPT_TYPES
 
 hipError_t launch_combine_backward(int T, int d, const float *dy, const Saved &y, const int32_t *row_of,
                                    const float *weights, void *dyp, void *dys, float *dg, bool f32_out, hipStream_t s) {

@@ -122,6 +122,22 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
     return m;
 }
 
+// v of another lane of the row of 16.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+}
+// Partner exchanges that combine 2, 4, 8, 16 neighbouring lanes when applied in
+// this order (the mirrors meet lanes that already hold their half's result).
+#define MOE_ROW_STEPS(STEP) STEP(0xB1) STEP(0x4E) STEP(0x141) STEP(0x140)
+
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#define STEP(C) v = max(v, dpp_u32<C>(v));
+    MOE_ROW_STEPS(STEP)
+#undef STEP
+    return v;
+}
+
 __device__ __forceinline__ float wave_max_f32(float v, int width) {
     for (int s = width / 2; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s, kWave));
     return v;

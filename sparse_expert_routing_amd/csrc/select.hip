@@ -223,10 +223,6 @@ __global__ __launch_bounds__(256) void k_select(SelectRule r, int T, const void 
 // -------------------------------------------------------- sixteen lanes per token
 
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
-}
-template <int CTRL>
 __device__ __forceinline__ float dpp_f32(float v) { return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v))); }
 // v of the lane N below in its row of 16, 0 for the first N.
 template <int N>
@@ -234,16 +230,6 @@ __device__ __forceinline__ uint32_t row_shr(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x110 + N, 0xf, 0xf, true);
 }
 
-// Partner exchanges that combine 2, 4, 8, 16 neighbouring lanes when applied in
-// this order (the mirrors meet lanes that already hold their half's result).
-#define MOE_ROW_STEPS(STEP) STEP(0xB1) STEP(0x4E) STEP(0x141) STEP(0x140)
-
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-#define STEP(C) v = max(v, dpp_u32<C>(v));
-    MOE_ROW_STEPS(STEP)
-#undef STEP
-    return v;
-}
 __device__ __forceinline__ uint32_t row_min(uint32_t v) {
 #define STEP(C) v = min(v, dpp_u32<C>(v));
     MOE_ROW_STEPS(STEP)
