@@ -60,7 +60,9 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&v)[4]) {
     }
 }
 
-// Eight consecutive values of a row (n of them inside it).
+// Eight values of a row: consecutive (VEC), or 16 columns apart, so that sixteen
+// lanes read and write neighbouring ones; n: columns of the row from the first
+// on (VEC: 8 or more).
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void load8(const void *src, int64_t at, int n, float (&v)[8]) {
     if (VEC && BF16) {
@@ -78,8 +80,8 @@ __device__ __forceinline__ void load8(const void *src, int64_t at, int n, float 
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = i >= n ? 0.f : BF16 ? bf16_to_f32(static_cast<const uint16_t *>(src)[at + i])
-                                       : static_cast<const float *>(src)[at + i];
+            v[i] = 16 * i >= n ? 0.f : BF16 ? bf16_to_f32(static_cast<const uint16_t *>(src)[at + 16 * i])
+                                            : static_cast<const float *>(src)[at + 16 * i];
     }
 }
 
@@ -96,9 +98,9 @@ __device__ __forceinline__ void store8(void *dst, int64_t at, int n, const float
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) {
-                if (BF16) static_cast<uint16_t *>(dst)[at + i] = (uint16_t)f32_to_bf16(v[i]);
-                else static_cast<float *>(dst)[at + i] = v[i];
+            if (16 * i < n) {
+                if (BF16) static_cast<uint16_t *>(dst)[at + 16 * i] = (uint16_t)f32_to_bf16(v[i]);
+                else static_cast<float *>(dst)[at + 16 * i] = v[i];
             }
     }
 }
@@ -117,11 +119,18 @@ __device__ __forceinline__ TilePlace place_of(int64_t base, int ntile) {
     return TilePlace{row, (int)(base - row * ntile)};
 }
 
-// Sixteen lanes per tile, eight values each; kUnroll tiles of a lane in flight.
-constexpr int kUnroll = 4;
+// Tiles of a lane in flight: four of a large dense array, so that a wave has enough
+// loads under way (131072 x 7168 bf16 to e4m3 and back: 1053 us with one, 986 with
+// four); one otherwise, where there are too few tiles to fill the card so (2408
+// tiles: 4 us a pass with one, 8 with four) or places cost registers.
+constexpr int kManyTiles = 65536;
+constexpr int unroll_of(bool flat) { return flat ? 4 : 1; }
+
+// Sixteen lanes per tile, eight values each.
 template <bool BF16, int FMT, bool VEC, bool FLAT>
 __global__ __launch_bounds__(256) void k_pack(int64_t rows, int cols, int ntile, const void *__restrict__ src, int64_t ld,
                                               uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    constexpr int kUnroll = unroll_of(FLAT);
     const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
     const int64_t tiles = rows * ntile, step = (int64_t)gridDim.x * (16 * kUnroll);
     for (int64_t base = (int64_t)blockIdx.x * (16 * kUnroll); base < tiles; base += step) {
@@ -133,13 +142,13 @@ __global__ __launch_bounds__(256) void k_pack(int64_t rows, int cols, int ntile,
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t tile = base + 16 * u + group;
             int64_t row = 0;
-            int c = sub * 8;
+            int c = VEC ? sub * 8 : sub;
             if (!FLAT) {
                 const uint32_t k = (uint32_t)(at.first + 16 * u + group), q = k / (uint32_t)ntile;
                 row = at.row + q;
                 c += (int)(k - q * ntile) * kTile;
             }
-            n[u] = tile < tiles ? (FLAT ? 8 : min(8, cols - c)) : 0;
+            n[u] = tile < tiles ? (FLAT ? 8 : min(kTile - (VEC ? 0 : sub), cols - c)) : 0;
             from[u] = FLAT ? tile * kTile + c : row * cols + c;
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
@@ -164,7 +173,7 @@ __global__ __launch_bounds__(256) void k_pack(int64_t rows, int cols, int ntile,
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i < n[u]) codes[from[u] + i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+                    if (16 * i < n[u]) codes[from[u] + 16 * i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
             }
         }
     }
@@ -173,6 +182,7 @@ __global__ __launch_bounds__(256) void k_pack(int64_t rows, int cols, int ntile,
 template <bool BF16, int FMT, bool VEC, bool FLAT>
 __global__ __launch_bounds__(256) void k_unpack(int64_t rows, int cols, int ntile, const uint8_t *__restrict__ codes,
                                                 const uint8_t *__restrict__ scales, void *__restrict__ dst, int64_t ld) {
+    constexpr int kUnroll = unroll_of(FLAT);
     const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
     const int64_t tiles = rows * ntile, step = (int64_t)gridDim.x * (16 * kUnroll);
     for (int64_t base = (int64_t)blockIdx.x * (16 * kUnroll); base < tiles; base += step) {
@@ -185,13 +195,13 @@ __global__ __launch_bounds__(256) void k_unpack(int64_t rows, int cols, int ntil
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t tile = base + 16 * u + group;
             int64_t row = 0;
-            int c = sub * 8;
+            int c = VEC ? sub * 8 : sub;
             if (!FLAT) {
                 const uint32_t k = (uint32_t)(at.first + 16 * u + group), q = k / (uint32_t)ntile;
                 row = at.row + q;
                 c += (int)(k - q * ntile) * kTile;
             }
-            n[u] = tile < tiles ? (FLAT ? 8 : min(8, cols - c)) : 0;
+            n[u] = tile < tiles ? (FLAT ? 8 : min(kTile - (VEC ? 0 : sub), cols - c)) : 0;
             const int64_t from = FLAT ? tile * kTile + c : row * cols + c;
             to[u] = FLAT ? from : row * ld + c;
             w[u] = uint2{0u, 0u};
@@ -203,7 +213,7 @@ __global__ __launch_bounds__(256) void k_unpack(int64_t rows, int cols, int ntil
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i < n[u]) (i < 4 ? w[u].x : w[u].y) |= (uint32_t)codes[from + i] << (8 * (i & 3));
+                    if (16 * i < n[u]) (i < 4 ? w[u].x : w[u].y) |= (uint32_t)codes[from + 16 * i] << (8 * (i & 3));
             }
         }
 #pragma unroll
@@ -330,8 +340,13 @@ bool vec_ok(const CkptArgs &a, const void *plain) {
     return a.cols % 8 == 0 && a.ld % (a.bf16 ? 8 : 4) == 0 && aligned(plain, 16) && aligned(a.codes, 8);
 }
 
-unsigned tile_grid(int64_t tiles) {
-    const int64_t n = (tiles + 16 * kUnroll - 1) / (16 * kUnroll);
+// Whether it is one run of many whole tiles.
+bool flat_ok(const CkptArgs &a) {
+    return a.cols % kTile == 0 && a.ld == a.cols && a.rows * (a.cols / kTile) >= kManyTiles;
+}
+
+unsigned tile_grid(int64_t tiles, bool flat) {
+    const int64_t per = 16 * unroll_of(flat), n = (tiles + per - 1) / per;
     return (unsigned)(n < (1 << 22) ? n : (1 << 22));
 }
 
@@ -354,16 +369,16 @@ unsigned tile_grid(int64_t tiles) {
 
 hipError_t launch_checkpoint_pack(const CkptArgs &a, hipStream_t s) {
     const int ntile = (a.cols + kTile - 1) / kTile;
-    const bool vec = vec_ok(a, a.src), flat = vec && a.cols % kTile == 0 && a.ld == a.cols;
-    const dim3 grid(tile_grid(a.rows * ntile)), block(256);
+    const bool vec = vec_ok(a, a.src), flat = vec && flat_ok(a);
+    const dim3 grid(tile_grid(a.rows * ntile, flat)), block(256);
     MOE_CKPT_VARIANTS(k_pack, grid, block, 0, s, a.rows, a.cols, ntile, a.src, a.ld, a.codes, a.scales);
     return hipGetLastError();
 }
 
 hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s) {
     const int ntile = (a.cols + kTile - 1) / kTile;
-    const bool vec = vec_ok(a, a.dst), flat = vec && a.cols % kTile == 0 && a.ld == a.cols;
-    const dim3 grid(tile_grid(a.rows * ntile)), block(256);
+    const bool vec = vec_ok(a, a.dst), flat = vec && flat_ok(a);
+    const dim3 grid(tile_grid(a.rows * ntile, flat)), block(256);
     MOE_CKPT_VARIANTS(k_unpack, grid, block, 0, s, a.rows, a.cols, ntile, a.codes, a.scales, a.dst, a.ld);
     return hipGetLastError();
 }
