@@ -270,12 +270,12 @@ __device__ __forceinline__ float from_key31(uint32_t k) { return f32_from_order_
 
 __device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(1.4426950408889634f * v); }
 
-// The Q experts from e0 on of a row that begins `at` elements into p, -inf behind
-// the last expert (a lane with no expert loads what lane 0 does).  vec: rows and
-// lanes begin at 16 bytes (or all of a lane's), and E is a multiple of Q.
+// The n <= Q experts from e0 on of a row that begins `at` elements into p, -inf
+// behind them (what is loaded there is another expert of the row).  vec: lanes
+// begin at 16 bytes (or all of a lane's), and n is Q or 0.
 template <int Q, bool BF16>
-__device__ __forceinline__ void load_row(const void *p, int64_t at, int e0, int E, bool vec, float (&l)[Q]) {
-    const int first = e0 < E ? e0 : 0;
+__device__ __forceinline__ void load_row(const void *p, int64_t at, int e0, int n, bool vec, float (&l)[Q]) {
+    const int first = n > 0 ? e0 : 0, last = n > 0 ? n - 1 : 0;
     const char *row = static_cast<const char *>(p) + (at + first) * (BF16 ? 2 : 4);
     if (vec && BF16) {
         constexpr int W = Q >= 8 ? 4 : 2;  // words per load
@@ -304,14 +304,10 @@ __device__ __forceinline__ void load_row(const void *p, int64_t at, int e0, int 
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) l[q] = load_logit<BF16>(row, min(first + q, E - 1) - first);
+        for (int q = 0; q < Q; ++q) l[q] = load_logit<BF16>(row, min(q, last));
     }
 #pragma unroll
-    for (int q = 0; q < Q; ++q) l[q] = e0 + q < E ? l[q] : -INFINITY;
-}
-template <int Q>
-__device__ __forceinline__ void load_f32(const float *p, int64_t at, int e0, int E, bool vec, float (&v)[Q]) {
-    load_row<Q, false>(p, at, e0, E, vec, v);
+    for (int q = 0; q < Q; ++q) l[q] = q < n ? l[q] : -INFINITY;
 }
 
 // Four experts per lane and load, 64 experts on for the next: the expert of a
@@ -355,20 +351,27 @@ bool spread_vec(int E, bool bf16, const void *logits, int64_t ld, const void *a,
            reinterpret_cast<uintptr_t>(a) % 16 == 0 && reinterpret_cast<uintptr_t>(b) % 16 == 0;
 }
 
-// Whether load_row can load whole vectors of rows ld apart, and of a dense fp32
-// row beside them.
-bool rows_vec(int Q, int E, bool bf16, const void *logits, int64_t ld, const void *a) {
-    const int64_t bytes = bf16 ? 2 : 4, step = Q * bytes < 16 ? Q * bytes : 16;
-    return E % Q == 0 && reinterpret_cast<uintptr_t>(logits) % step == 0 && ld * bytes % step == 0 &&
-           reinterpret_cast<uintptr_t>(a) % 16 == 0;
+// How a row's groups lie over sixteen lanes.
+struct LaneMap {
+    int groups, per;          // groups of so many experts
+    int lanes, shift;         // lanes per group, a power of two, and its logarithm
+    int run;                  // experts per lane, the group's last lane with what is left
+};
+LaneMap lane_map(const SelectRule &r) {
+    LaneMap m{r.topk_group < r.n_group ? r.n_group : 1, 0, 16, 4, 0};
+    m.per = r.E / m.groups;
+    while (m.lanes > 1 && m.lanes * m.groups > 16) m.lanes /= 2, --m.shift;
+    m.run = (m.per + m.lanes - 1) / m.lanes;
+    return m;
 }
 
 // What the keys are made of: bf16 logits with the id in the low bits (no two
 // alike, nothing rounded), fp32 logits, or the biased fp32 scores.
 enum { KEY_BF16 = 0, KEY_F32 = 1, KEY_SCORE = 2 };
 
-// Sixteen lanes per token, four tokens per wave; lane i holds the Q experts from
-// Q i on.  Keys are 31-bit unsigned numbers (0: not an expert, or its group is
+// Sixteen lanes per token, four tokens per wave.  A lane holds up to Q neighbouring
+// experts of one group, each group has 1, 2, 4, 8 or 16 neighbouring lanes (LaneMap;
+// all experts are one group where none is closed).  Keys are 31-bit unsigned numbers (0: not an expert, or its group is
 // closed), so that with the largest key below m wanted, k - m as an unsigned
 // number is at least 2^31 for a key below m and less for the others, and the
 // largest difference is the answer: one subtraction and half a three-way maximum
@@ -383,7 +386,7 @@ enum { KEY_BF16 = 0, KEY_F32 = 1, KEY_SCORE = 2 };
 //
 // 16384 tokens, 256 experts in 8 groups, 8 chosen: see launch_select.
 template <int Q, int KEY, bool BF16>
-__global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per_group, bool vec, int T,
+__global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, bool vec, int T,
                                                      const void *__restrict__ logits, int64_t ld,
                                                      const float *__restrict__ bias, int32_t *__restrict__ idx,
                                                      float *__restrict__ wts) {
@@ -395,10 +398,11 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
     if (t0 >= T) return;
     const int64_t t = min(t0 + (lane >> 4), (int64_t)T - 1);
     const bool mine = t0 + (lane >> 4) < T;
-    const int e0 = sub * Q;
+    const int group = sub >> map.shift, e1 = (sub & (map.lanes - 1)) * map.run;  // in the group
+    const int e0 = group * map.per + e1, n = group < map.groups ? min(map.run, map.per - e1) : 0;
     float l[Q], b[Q];
-    load_row<Q, BF16>(logits, t * ld, e0, r.E, vec, l);
-    if (KEY == KEY_SCORE) load_f32<Q>(bias, 0, e0, r.E, vec, b);
+    load_row<Q, BF16>(logits, t * ld, e0, n, vec, l);
+    if (KEY == KEY_SCORE) load_row<Q, false>(bias, 0, e0, n, vec, b);
     // a NaN ranks behind every number: the 64-bit code's business
     bool doubt = false;
 #pragma unroll
@@ -429,7 +433,7 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         if (KEY == KEY_SCORE) {
-            b[q] += s[q];
+            b[q] += s[q];  // (-inf behind the last expert)
             doubt |= b[q] != b[q];
             key[q] = key31(b[q]);
         } else if (KEY == KEY_F32) {
@@ -437,7 +441,7 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
         } else {
             key[q] = ((f32_order_key(l[q] + 0.f) >> 16) << 15) | (uint32_t)(0x7fff - (e0 + q));
         }
-        key[q] = e0 + q < r.E ? key[q] : 0;
+        key[q] = q < n ? key[q] : 0;
     }
     const float near = r.softmax ? 7.62939453125e-6f : 9.5367431640625e-7f;  // 2^-17, 2^-20
 
@@ -448,30 +452,31 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, int lanes_per
             float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                const float v = KEY == KEY_SCORE ? b[q] : s[q];
+                const float v = KEY == KEY_SCORE ? b[q] : q < n ? s[q] : -INFINITY;
                 a2 = __builtin_amdgcn_fmed3f(a1, a2, v);  // a2 <= a1: the second of the three
                 a1 = fmaxf(a1, v);
             }
 #define STEP(C, LANES)                                         \
-    if (lanes_per_group >= LANES) {                            \
+    if (map.lanes >= LANES) {                            \
         const float o1 = dpp_f32<C>(a1), o2 = dpp_f32<C>(a2);  \
         a2 = fmaxf(fminf(a1, o1), fmaxf(a2, o2));              \
         a1 = fmaxf(a1, o1);                                    \
     }
             STEP(0xB1, 2) STEP(0x4E, 4) STEP(0x141, 8) STEP(0x140, 16)
 #undef STEP
-            doubt |= a1 + a2 != a1 + a2;
-            g = e0 < r.E ? key31(a1 + a2) : 0;
+            if (map.per == 1) a2 = 0.f;
+            doubt |= group < map.groups && a1 + a2 != a1 + a2;
+            g = group < map.groups ? key31(a1 + a2) : 0;
         } else {
             g = key[0];
 #pragma unroll
             for (int q = 1; q < Q; ++q) g = max(g, key[q]);
 #define STEP(C, LANES) \
-    if (lanes_per_group >= LANES) g = max(g, dpp_u32<C>(g));
+    if (map.lanes >= LANES) g = max(g, dpp_u32<C>(g));
             STEP(0xB1, 2) STEP(0x4E, 4) STEP(0x141, 8) STEP(0x140, 16)
 #undef STEP
         }
-        const int want = r.topk_group * lanes_per_group;
+        const int want = r.topk_group * map.lanes;
         const bool is_open = row_rank(g) < want;
         // equal groups at the border open together
         doubt |= row_add(is_open ? 1u : 0u) != (uint32_t)want;
@@ -854,31 +859,29 @@ int balance_blocks(int T) { return (T + kBalanceTokens - 1) / kBalanceTokens; }
         else LAUNCH(1024 / LANES);                       \
     } while (0)
 
-// Lanes per group of k_select_fast<Q>, 0 where its exchanges do not fit the
-// groups: a group has to be 1, 2, 4, 8 or 16 whole lanes.
-static int group_lanes(const SelectRule &r, int Q) {
-    if (r.topk_group == r.n_group) return 16;  // no group is closed
-    const int per = r.E / r.n_group, n = per / Q;
-    return per % Q == 0 && n <= 16 && (n & (n - 1)) == 0 ? n : 0;
-}
-
 hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
     const SelectRule &r = a.rule;
     const dim3 block(256);
-    const int Q = r.E <= 64 ? 4 : r.E <= 128 ? 8 : r.E <= 256 ? 16 : 32;
-    const int lanes = r.E <= 512 ? group_lanes(r, Q) : 0;
-    if (lanes) {
+    // Sixteen lanes hold up to 32 experts each; more of them, or more than 16 groups,
+    // are left to the wave per token.
+    LaneMap map = lane_map(r);
+    if (map.lanes * map.groups <= 16 && map.run <= 32) {
         const dim3 grid((unsigned)(((int64_t)a.T + 15) / 16));
-        const bool vec = rows_vec(Q, r.E, a.bf16, a.logits, a.ld, a.bias);
+        const int Q = map.run <= 4 ? 4 : map.run <= 8 ? 8 : map.run <= 16 ? 16 : 32;
+        // whole vectors: a group's lanes all full, or empty
+        const int64_t bytes = a.bf16 ? 2 : 4, step = Q * bytes < 16 ? Q * bytes : 16;
+        const bool vec = map.per % Q == 0 && reinterpret_cast<uintptr_t>(a.logits) % step == 0 &&
+                         a.ld * bytes % step == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+        if (vec) map.run = Q;
 #define FAST(QQ)                                                                                                     \
     do {                                                                                                             \
-        if (a.bias && a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, true>), grid, block, 0, s, r, lanes,   \
+        if (a.bias && a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, true>), grid, block, 0, s, r, map,     \
                                                  vec, a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                \
-        else if (a.bias) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, false>), grid, block, 0, s, r, lanes, vec, \
+        else if (a.bias) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, false>), grid, block, 0, s, r, map, vec,   \
                                             a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                          \
-        else if (a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_BF16, true>), grid, block, 0, s, r, lanes, vec,   \
+        else if (a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_BF16, true>), grid, block, 0, s, r, map, vec,     \
                                             a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                          \
-        else hipLaunchKernelGGL((k_select_fast<QQ, KEY_F32, false>), grid, block, 0, s, r, lanes, vec, a.T, a.logits, \
+        else hipLaunchKernelGGL((k_select_fast<QQ, KEY_F32, false>), grid, block, 0, s, r, map, vec, a.T, a.logits, \
                                 a.ld, a.bias, a.idx, a.weights);                                                     \
     } while (0)
         if (Q == 4) FAST(4);
