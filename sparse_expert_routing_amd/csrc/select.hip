@@ -557,22 +557,28 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
 
 // ------------------------------------------------------------- the sequences
 
-// How many of the sequences [0, n) end at or before token t (their ends are
-// ascending): the sequence that holds t, or n behind the last one.  Sixty-four
-// ends are compared at a time.
-__device__ __forceinline__ int sequence_of(const int32_t *__restrict__ off, int n, int t) {
+// How many i of [0, n) have holds(i), which holds for the first ones and no
+// others.  The wave looks at sixty-four of them at a time.
+template <typename F>
+__device__ __forceinline__ int count_leading(int n, F holds) {
     const int lane = threadIdx.x & 63;
     int lo = 0;
     while (n > 64) {
         const int step = (n + 63) / 64;
         const int i = min(lane * step + step, n) - 1;
-        const int full = __popcll(__ballot(off[1 + lo + i] <= t));
+        const int full = __popcll(__ballot(holds(lo + i)));
         if (full == 64) return lo + n;
         lo += full * step;
         n = min(step, n - full * step);
         if (n <= 0) return lo;
     }
-    return lo + __popcll(__ballot(lane < n && off[1 + lo + min(lane, n - 1)] <= t));
+    return lo + __popcll(__ballot(lane < n && holds(lo + min(lane, n - 1))));
+}
+
+// The sequence of [0, n) that holds token t, or n behind the last one: how many
+// end at or before t.
+__device__ __forceinline__ int sequence_of(const int32_t *__restrict__ off, int n, int t) {
+    return count_leading(n, [&](int i) { return off[1 + i] <= t; });
 }
 
 // The gradient with respect to the logits of one token:
@@ -730,11 +736,11 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
     }
 }
 
-// Partial sums of the balance loss: a workgroup takes kBalanceTokens tokens and
-// walks the sequences that lie in them; each (workgroup, sequence) pair owns
-// slot workgroup + sequence (ascending in both, so no two share one), where it
-// leaves the sum of the tokens' shares and the count of choices per expert.
-// Sixteen lanes per token, each lane sums its own experts.
+// Partial sums of the balance loss.  The tokens are cut at every kBalanceTokens and
+// at every sequence: the piece of sequence s that lies in the c-th kBalanceTokens
+// tokens is number c + s (ascending in both, so no two share one), and workgroup
+// and slot of that number leave the sum of its tokens' shares and the count of
+// choices per expert.  Sixteen lanes per token, each lane sums its own experts.
 template <int Q, bool BF16>
 __global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, int T, const void *__restrict__ logits,
                                                       int64_t ld, const int32_t *__restrict__ idx,
@@ -743,58 +749,56 @@ __global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, in
     __shared__ float share[8][16 * Q];
     __shared__ int32_t hist[16 * Q];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane & 15;
-    const int t1 = (int)min((int64_t)(blockIdx.x + 1) * kBalanceTokens, (int64_t)T);
-    int t = max((int)((int64_t)blockIdx.x * kBalanceTokens), seq[0]);
-    while (t < t1) {
-        const int s = sequence_of(seq, n_seq, t);
-        if (s >= n_seq) break;
-        const int end = max(t + 1, min(t1, seq[s + 1]));
-        for (int e = tid; e < 16 * Q; e += 512) hist[e] = 0;
-        float sum[Q];
+    const int64_t slot = blockIdx.x;
+    // the last sequence whose first piece has this number or less
+    const int s = count_leading(n_seq, [&](int i) { return (int64_t)max(seq[i], 0) / kBalanceTokens + i <= slot; }) - 1;
+    if (s < 0) return;
+    const int64_t c0 = (slot - s) * kBalanceTokens;
+    const int t = (int)min(max(c0, (int64_t)max(seq[s], 0)), (int64_t)T);
+    const int end = (int)min(min(c0 + kBalanceTokens, (int64_t)max(seq[s + 1], 0)), (int64_t)T);
+    if (t >= end) return;
+    for (int e = tid; e < 16 * Q; e += 512) hist[e] = 0;
+    float sum[Q];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) sum[q] = 0.f;
-        for (int u0 = t + 4 * wave; u0 < end; u0 += 32) {
-            const int u = u0 + (lane >> 4);
-            float p[Q], m = -INFINITY, total = 0.f;
-            load_spread<Q, BF16>(logits, (int64_t)min(u, end - 1) * ld, sub, r.E, vec, -INFINITY, p);
-            if (r.softmax) {
+    for (int q = 0; q < Q; ++q) sum[q] = 0.f;
+    for (int u0 = t + 4 * wave; u0 < end; u0 += 32) {
+        const int u = u0 + (lane >> 4);
+        float p[Q], m = -INFINITY, total = 0.f;
+        load_spread<Q, BF16>(logits, (int64_t)min(u, end - 1) * ld, sub, r.E, vec, -INFINITY, p);
+        if (r.softmax) {
 #pragma unroll
-                for (int q = 0; q < Q; ++q) m = fmaxf(m, p[q]);
-                m = row_maxf(m);
-            }
-#pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                p[q] = r.softmax ? (m == -INFINITY ? 0.f : fast_exp(p[q] - m)) : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
-                total += p[q];
-            }
-            total = row_sum(total);
-            const float c = u < end && total != 0.f ? 1.f / total : 0.f;
-#pragma unroll
-            for (int q = 0; q < Q; ++q) sum[q] += p[q] * c;
+            for (int q = 0; q < Q; ++q) m = fmaxf(m, p[q]);
+            m = row_maxf(m);
         }
-        // the wave's four rows, then the waves, in a fixed order
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            sum[q] += __shfl_xor(sum[q], 16, kWave);
-            sum[q] += __shfl_xor(sum[q], 32, kWave);
-            if (lane < 16) share[wave][spread(sub, q)] = sum[q];
+            p[q] = r.softmax ? (m == -INFINITY ? 0.f : fast_exp(p[q] - m)) : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
+            total += p[q];
         }
-        __syncthreads();
-        for (int i = t * r.k + tid; i < end * r.k; i += 512) {
-            const int e = idx[i];
-            if (e >= 0 && e < r.E) atomicAdd(&hist[e], 1);
-        }
-        __syncthreads();
-        const int64_t slot = (int64_t)blockIdx.x + s;
-        for (int e = tid; e < r.E; e += 512) {
-            float v = share[0][e];
+        total = row_sum(total);
+        const float c = u < end && total != 0.f ? 1.f / total : 0.f;
 #pragma unroll
-            for (int w = 1; w < 8; ++w) v += share[w][e];
-            part[slot * r.E + e] = v;
-            count[slot * r.E + e] = hist[e];
-        }
-        __syncthreads();
-        t = end;
+        for (int q = 0; q < Q; ++q) sum[q] += p[q] * c;
+    }
+    // the wave's four rows, then the waves, in a fixed order
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        sum[q] += __shfl_xor(sum[q], 16, kWave);
+        sum[q] += __shfl_xor(sum[q], 32, kWave);
+        if (lane < 16) share[wave][spread(sub, q)] = sum[q];
+    }
+    __syncthreads();
+    for (int i = t * r.k + tid; i < end * r.k; i += 512) {
+        const int e = idx[i];
+        if (e >= 0 && e < r.E) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    for (int e = tid; e < r.E; e += 512) {
+        float v = share[0][e];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) v += share[w][e];
+        part[slot * r.E + e] = v;
+        count[slot * r.E + e] = hist[e];
     }
 }
 
@@ -927,7 +931,7 @@ hipError_t launch_balance_loss(const BalanceArgs &a, void *ws, hipStream_t s) {
     const size_t slots = (size_t)balance_blocks(a.T) + a.n_seq;
     float *part = static_cast<float *>(ws);
     int32_t *count = reinterpret_cast<int32_t *>(part + slots * a.rule.E);
-    const dim3 grid(balance_blocks(a.T)), block(512);
+    const dim3 grid((unsigned)slots), block(512);
 #define GO(Q)                                                                                                         \
     do {                                                                                                              \
         const bool vec = spread_vec(a.rule.E, a.bf16, a.logits, a.ld, nullptr, nullptr);                              \
