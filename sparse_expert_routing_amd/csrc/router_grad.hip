@@ -80,15 +80,30 @@ struct RgWs {
     size_t bytes;
 };
 
-// Splits of dw's K = T range: about one workgroup per CU, eight stages at least
-// each.  Neighbouring workgroups take different splits, so with a multiple of 8
-// each XCD works on its own tokens and keeps their dl terms in its L2.
-int dw_splits(int T, int d) {
-    const int tiles = (d + 255) / 256, stages = (T + kStageK - 1) / kStageK;
-    int S = 256 / tiles;
-    if (S > 8) S = S / 8 * 8;
+// How the two products are cut into workgroups.  Large problems: 128 columns per dx
+// block and 256 per dw block, about one of each per CU.  Where those are too few
+// to fill the card, 32 and 64.
+struct Cut {
+    bool small;
+    int dx_cols, dw_cols, dx_split, dw_split;
+};
+Cut cut_of(int T, int d) {
+    Cut c{};
+    const int rounds = (T + 255) / 256, stages = (T + kStageK - 1) / kStageK;
+    c.small = (int64_t)((d + 127) / 128) * rounds < 128;
+    c.dx_cols = c.small ? 32 : 128;
+    c.dw_cols = c.small ? 64 : 256;
+    const int dx_tiles = (d + c.dx_cols - 1) / c.dx_cols, dw_tiles = (d + c.dw_cols - 1) / c.dw_cols;
+    // dx: its 8 waves have one chunk of 32 tokens at least
+    c.dx_split = 256 / dx_tiles;
+    c.dx_split = c.dx_split < 1 ? 1 : c.dx_split > rounds ? rounds : c.dx_split;
+    // dw: eight stages at least.  Neighbouring workgroups take different splits, so with a
+    // multiple of 8 each XCD works on its own tokens and keeps their dl terms in its L2.
+    c.dw_split = 256 / dw_tiles;
+    if (c.dw_split > 8) c.dw_split = c.dw_split / 8 * 8;
     const int most = (stages + 7) / 8;
-    return S < 1 ? 1 : S > most ? most : S;
+    c.dw_split = c.dw_split < 1 ? 1 : c.dw_split > most ? most : c.dw_split;
+    return c;
 }
 
 RgWs carve(char *base, int T, int d, bool x_bf16) {
@@ -100,7 +115,7 @@ RgWs carve(char *base, int T, int d, bool x_bf16) {
         return p;
     };
     w.Tp = (T + 31) / 32 * 32;
-    w.S = dw_splits(T, d);
+    w.S = cut_of(T, d).dw_split;
     w.dlh = reinterpret_cast<uint16_t *>(take((size_t)2 * w.Tp * kE * 2));
     w.er = reinterpret_cast<int32_t *>(take((size_t)w.Tp * 4));
     w.wh = reinterpret_cast<uint16_t *>(take((size_t)2 * d * kE * 2));
@@ -220,34 +235,34 @@ __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, 
 
 // ------------------------------------------------------------------- dx
 
-constexpr int kDxN = 128;  // columns per workgroup
-
 // Position of 16-byte piece c of row r in an LDS tile of 512-byte rows: rows
 // that are read together lie in different banks.
 __device__ __forceinline__ int piece512(int r, int c) { return r * kE + ((c ^ (r & 15)) * 8); }
 
-// A workgroup keeps its 128 columns' terms of w in LDS (128 KB) and its 8 waves
+// A workgroup keeps its 32 NJ columns' terms of w in LDS (32 NJ KB) and its 8 waves
 // walk 32-token chunks: their dl terms come straight from memory (each wave
 // has its own rows, so LDS would not save a read), laid out so that a fragment is
-// 1 KB in a row; there is no barrier in the loop.  32x32x16 tiles, 4 per wave; lane: column n, so a store is 128 bytes of a row.
-__global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, const int32_t *__restrict__ er,
-                                                  const float *dx_in, float *dx) {
-    __shared__ __attribute__((aligned(1024))) uint16_t sw[2 * kDxN * kE];
+// 1 KB in a row; there is no barrier in the loop.  32x32x16 tiles, NJ per wave; lane: column n, so a store is 128 bytes
+// of a row.  Block z of S, tile y.
+template <int NJ>
+__device__ __forceinline__ void dx_block(int T, int d, const RgWs &ws, const int32_t *__restrict__ er,
+                                         const float *dx_in, float *dx, uint16_t *sw, int z, int S, int y) {
+    constexpr int kDxN = 32 * NJ;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.y * kDxN;
-    // 256 rows (term, n) of 512 bytes, two per load instruction
+    const int n0 = y * kDxN;
+    // 64 NJ rows (term, n) of 512 bytes, two per load instruction
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int r = 2 * (wave * 16 + i) + g, n = min(n0 + (r & (kDxN - 1)), d - 1);
+    for (int i = 0; i < 4 * NJ; ++i) {
+        const int r = 2 * (wave * 4 * NJ + i) + g, n = min(n0 + (r & (kDxN - 1)), d - 1);
         const int c = (lane & 31) ^ (r & 15);
-        dma16(ws.wh + ((int64_t)(r / kDxN) * d + n) * kE + 8 * c, sw + 2 * (wave * 16 + i) * kE);
+        dma16(ws.wh + ((int64_t)(r / kDxN) * d + n) * kE + 8 * c, sw + 2 * (wave * 4 * NJ + i) * kE);
     }
-    const int chunks = (T + 31) / 32, S = gridDim.x, z = blockIdx.x;
+    const int chunks = (T + 31) / 32;
     const int c0 = (int)((int64_t)chunks * z / S), c1 = (int)((int64_t)chunks * (z + 1) / S);
-    int ec[4];
+    int ec[NJ];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) ec[j] = ws.ec[min(n0 + 32 * j + (lane & 31), d - 1)];
+    for (int j = 0; j < NJ; ++j) ec[j] = ws.ec[min(n0 + 32 * j + (lane & 31), d - 1)];
     all_landed();
     // LDS: row 32 j + lane % 32 of term m at + 16 KB j + 64 KB m, piece 2 ks + g by one xor
     const uint32_t row_off = (uint32_t)piece512(lane & 31, g);
@@ -260,13 +275,13 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
             v[1][s] = *reinterpret_cast<const f16x8 *>(p + 32 * kE + s * 512);
         }
     };
-    f32x16 acc[4];
+    f32x16 acc[NJ];
     auto quarter = [&](int q, const f16x8 (&v)[2][4]) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const uint16_t *h = sw + (row_off ^ (uint32_t)(16 * (4 * q + s))), *m = h + kDxN * kE;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < NJ; ++j) {
                 const f16x8 bh = *reinterpret_cast<const f16x8 *>(h + 32 * j * kE);
                 const f16x8 bm = *reinterpret_cast<const f16x8 *>(m + 32 * j * kE);
                 acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[1][s], bh, acc[j], 0, 0, 0);
@@ -283,7 +298,7 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
     }
     for (int ch = c0 + wave; ch < c1; ch += 8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = f32x16{};
+        for (int j = 0; j < NJ; ++j) acc[j] = f32x16{};
         quarter(0, a[0]);
         __builtin_amdgcn_sched_barrier(0);
         load(ch, 2, a[0]);
@@ -295,20 +310,20 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
         const int t0 = ch * 32 + 4 * g, n = n0 + (lane & 31);
         const bool whole = ch * 32 + 32 <= T && n0 + kDxN <= d;
         const int64_t at0 = (int64_t)t0 * d + n;
-        f32x16 in[4];
+        f32x16 in[NJ];
         if (dx_in == nullptr) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) in[j] = f32x16{};
+            for (int j = 0; j < NJ; ++j) in[j] = f32x16{};
         } else if (whole) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) in[j][i] = dx_in[at0 + (int64_t)(8 * (i >> 2) + (i & 3)) * d + 32 * j];
+                for (int j = 0; j < NJ; ++j) in[j][i] = dx_in[at0 + (int64_t)(8 * (i >> 2) + (i & 3)) * d + 32 * j];
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < NJ; ++j) {
                     const int row = 8 * (i >> 2) + (i & 3);
                     in[j][i] = t0 + row < T && n + 32 * j < d ? dx_in[at0 + (int64_t)row * d + 32 * j] : 0.f;
                 }
@@ -328,18 +343,18 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
                 const int lo = er[ch * 32 + 8 * q + r], hi = er[ch * 32 + 8 * q + 4 + r];  // wave-uniform
                 const int e = g ? hi : lo;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j][4 * q + r] = ldexpf(acc[j][4 * q + r], e + ec[j]) + in[j][4 * q + r];
+                for (int j = 0; j < NJ; ++j) acc[j][4 * q + r] = ldexpf(acc[j][4 * q + r], e + ec[j]) + in[j][4 * q + r];
             }
         if (whole) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) dx[at0 + (int64_t)(8 * (i >> 2) + (i & 3)) * d + 32 * j] = acc[j][i];
+                for (int j = 0; j < NJ; ++j) dx[at0 + (int64_t)(8 * (i >> 2) + (i & 3)) * d + 32 * j] = acc[j][i];
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < NJ; ++j) {
                     const int row = 8 * (i >> 2) + (i & 3);
                     if (t0 + row < T && n + 32 * j < d) dx[at0 + (int64_t)row * d + 32 * j] = acc[j][i];
                 }
@@ -348,8 +363,6 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
 }
 
 // ------------------------------------------------------------------- dw
-
-constexpr int kDwN = 256;  // columns per workgroup
 
 // A 16-byte load per lane into LDS, written as assembly: the compiler sees no
 // LDS write, so it does not wait for the loads in flight before the LDS reads
@@ -361,29 +374,38 @@ __device__ __forceinline__ void dma16_unseen(const void *src, const uint16_t *ld
     asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(to) : "memory");
 }
 
-// 256 experts x 256 columns per workgroup, 8 waves of 64 x 128, stages of K = 16
-// in a ring of 5 (NX = 1: three terms of dl^T, 24 KB, and x, 8 KB: 160 KB), four of
-// them in flight.  x lies K-major and is read with transposing LDS reads: within
-// each 16 lanes, lane 4a + c receives element c of the 8 bytes that lanes a, a+4,
-// a+8, a+12 point at; its 16-byte piece c of row k sits at c ^ 4 (k % 4).
+// 256 experts x 64 NB columns per workgroup, 8 waves of 64 x 32 NB, stages of K = 16
+// in a ring of 5 (NB = 4, bf16 x: three terms of dl^T, 24 KB, and x, 8 KB: 160 KB),
+// four of them in flight.  x lies K-major and is read with transposing LDS reads:
+// within each 16 lanes, lane 4a + c receives element c of the 8 bytes that lanes a,
+// a+4, a+8, a+12 point at; its 16-byte piece c of row k sits at c ^ 4 (k % 4) (rows
+// of 512 bytes) or c ^ 2 (k % 4) (128 bytes, where two rows share the banks).
+template <int NX, int NB>
+constexpr int dw_stage() { return 3 * kE * kStageK + NX * kStageK * 64 * NB; }  // elements
 template <int NX>
-__global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, const uint16_t *__restrict__ x,
-                                                  float *__restrict__ out) {
+constexpr int dw_ring() { return NX == 1 ? 5 : 3; }
+template <int NX, int NB>
+__device__ __forceinline__ void dw_block(int T, int d, const RgWs &ws, const uint16_t *__restrict__ x,
+                                         float *__restrict__ out, uint16_t *smem, int z, int S, int y) {
+    constexpr int kDwN = 64 * NB, kPieces = kDwN / 8, kTurn = NB == 4 ? 4 : 2;
     constexpr int kA = 3 * kE * kStageK, kX = kStageK * kDwN;  // elements per stage
-    constexpr int kBuf = kA + NX * kX, kRing = NX == 1 ? 5 : 3;
-    constexpr int kLoads = 3 + NX;  // per wave and stage
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[kRing * kBuf];
+    constexpr int kBuf = kA + NX * kX, kRing = dw_ring<NX>();
+    constexpr int kRowsPer = 64 / kPieces;                // rows of x per load instruction
+    constexpr int kXWaves = kStageK / kRowsPer;           // waves that load x
+    constexpr int kLoads = 3 + NX;                        // per wave and stage
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int S = ws.S, z = blockIdx.x % S, n0 = (blockIdx.x / S) * kDwN;
+    const int n0 = y * kDwN;
     const int stages = ws.Tp / kStageK;
     const int s0 = (int)((int64_t)stages * z / S), s1 = (int)((int64_t)stages * (z + 1) / S);
     out += (int64_t)z * kE * d;
 
-    // A: 24 KB in a row, 3 KB per wave; x: row 2 wave + g of each term
+    // A: 24 KB in a row, 3 KB per wave; x: some rows of each term (waves behind the last
+    // row load the first ones' again, so that every wave counts the same loads)
     const uint16_t *asrc = ws.dlt + wave * 3 * 512 + 8 * lane;
-    const int xk = 2 * wave + g, xn = min(n0 + 8 * ((lane & 31) ^ (4 * (xk & 3))), d - 8);
+    const int xblk = wave % kXWaves, xk = kRowsPer * xblk + lane / kPieces;
+    const int xn = min(n0 + 8 * ((lane % kPieces) ^ (kTurn * (xk & 3))), d - 8);
     auto issue = [&](int st, uint16_t *to) {
         st = min(st, s1 - 1);  // behind the end the last stage again, never read: the loads stay countable
 #pragma unroll
@@ -392,13 +414,13 @@ __global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, c
         const int64_t t = min(st * kStageK + xk, T - 1);
 #pragma unroll
         for (int u = 0; u < NX; ++u)
-            dma16_unseen(x + (u * (int64_t)T + t) * d + xn, to + kA + u * kX + 2 * wave * kDwN);
+            dma16_unseen(x + (u * (int64_t)T + t) * d + xn, to + kA + u * kX + kRowsPer * xblk * kDwN);
     };
-    f32x16 acc[2][4];
+    f32x16 acc[2][NB];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+        for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
     const int h = lane >> 4, b = lane & 15;
     const int bk = 8 * (h >> 1) + (b >> 2);  // + 4 for the second read
     auto step = [&](const uint16_t *st) {
@@ -410,11 +432,11 @@ __global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, c
                 a[m][i] = *reinterpret_cast<const bf16x8 *>(st + m * kE * kStageK +
                                                             piece32(wm * 64 + 32 * i + (lane & 31), g));
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int u = 0; u < NX; ++u) {
-                const int col = wn * 128 + 32 * j + 16 * (h & 1) + 4 * (b & 3);
-                const uint16_t *p = st + kA + u * kX + bk * kDwN + ((((col >> 3) ^ (4 * (bk & 3))) << 3) | (col & 7));
+                const int col = wn * 32 * NB + 32 * j + 16 * (h & 1) + 4 * (b & 3);
+                const uint16_t *p = st + kA + u * kX + bk * kDwN + ((((col >> 3) ^ (kTurn * (bk & 3))) << 3) | (col & 7));
                 const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)p);
                 const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(p + 4 * kDwN));
                 const bf16x8 xb = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -442,12 +464,12 @@ __global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, c
         next = next == kRing - 1 ? 0 : next + 1;
     }
     all_landed();  // nothing is on its way into LDS when the workgroup ends
-    // lane: column n0 + 128 wn + 32 j + lane % 32, experts 64 wm + 32 i + 8 q + 4 g + r
+    // lane: column n0 + 32 NB wn + 32 j + lane % 32, experts 64 wm + 32 i + 8 q + 4 g + r
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + wn * 128 + 32 * j + (lane & 31);
+        for (int j = 0; j < NB; ++j) {
+            const int n = n0 + wn * 32 * NB + 32 * j + (lane & 31);
             if (n >= d) continue;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -455,6 +477,34 @@ __global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, c
                 for (int r = 0; r < 4; ++r)
                     out[(int64_t)(wm * 64 + 32 * i + 8 * q + 4 * g + r) * d + n] = acc[i][j][4 * q + r];
         }
+}
+
+// Both products in one launch, so that dx, which waits for memory, and dw, which
+// keeps the matrix cores busy, run side by side: workgroups in turns of eight (an
+// XCD each) as long as both have some left.
+struct RgGrid {
+    int dx_split, dx_tiles, dw_split, dw_tiles;
+};
+template <int NX, int NJ, int NB>
+__global__ __launch_bounds__(512, 1) void k_rg_products(int T, int d, const RgWs ws, const RgGrid p,
+                                                        const int32_t *__restrict__ er, const float *dx_in, float *dx,
+                                                        const uint16_t *__restrict__ x, float *__restrict__ out) {
+    constexpr int kDwLds = dw_ring<NX>() * dw_stage<NX, NB>(), kDxLds = 2 * 32 * NJ * kE;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[kDwLds > kDxLds ? kDwLds : kDxLds];
+    const int ndx = p.dx_split * p.dx_tiles, ndw = p.dw_split * p.dw_tiles;
+    const int b = blockIdx.x, turns = min(ndx, ndw) / 8;
+    int at;
+    bool is_dx;
+    if (b < 16 * turns) {
+        is_dx = ((b >> 3) & 1) == 0;
+        at = (b >> 4) * 8 + (b & 7);
+    } else {
+        at = b - 8 * turns;
+        is_dx = at < ndx;
+        if (!is_dx) at = b - ndx;
+    }
+    if (is_dx) dx_block<NJ>(T, d, ws, er, dx_in, dx, smem, at % p.dx_split, p.dx_split, at / p.dx_split);
+    else dw_block<NX, NB>(T, d, ws, x, out, smem, at % p.dw_split, p.dw_split, at / p.dw_split);
 }
 
 // dw = the S partial sums added in order, 4 values per thread.
@@ -480,16 +530,21 @@ hipError_t launch_router_grad(const RouterGradArgs &a, void *workspace, hipStrea
     if (nw + nt + nx > INT32_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_rg_split, dim3((unsigned)(nw + nt + nx)), dim3(256), 0, s, T, d, nw, nt, a.w, a.dlogits,
                        static_cast<const float *>(a.x_bf16 ? nullptr : a.x), ws);
-    // dx: about one workgroup per CU, at least one round of 8 chunks each
-    const int ntile = (d + kDxN - 1) / kDxN, rounds = (T + 255) / 256;
-    const int S = 256 / ntile < 1 ? 1 : 256 / ntile > rounds ? rounds : 256 / ntile;
-    hipLaunchKernelGGL(k_rg_dx, dim3(S, ntile), dim3(512), 0, s, T, d, ws, ws.er, a.dx_in, a.dx);
+    const Cut c = cut_of(T, d);
+    const RgGrid p{c.dx_split, (d + c.dx_cols - 1) / c.dx_cols, c.dw_split, (d + c.dw_cols - 1) / c.dw_cols};
+    const dim3 grid((unsigned)(p.dx_split * p.dx_tiles + p.dw_split * p.dw_tiles)), block(512);
     float *out = ws.S == 1 ? a.dw : ws.part;
-    const dim3 grid((unsigned)(ws.S * ((d + kDwN - 1) / kDwN)));
-    if (a.x_bf16)
-        hipLaunchKernelGGL(k_rg_dw<1>, grid, dim3(512), 0, s, T, d, ws, static_cast<const uint16_t *>(a.x), out);
-    else
-        hipLaunchKernelGGL(k_rg_dw<3>, grid, dim3(512), 0, s, T, d, ws, ws.xs, out);
+    const uint16_t *x = a.x_bf16 ? static_cast<const uint16_t *>(a.x) : ws.xs;
+#define GO(NX)                                                                                                      \
+    do {                                                                                                            \
+        if (c.small) hipLaunchKernelGGL((k_rg_products<NX, 1, 1>), grid, block, 0, s, T, d, ws, p, ws.er, a.dx_in,  \
+                                        a.dx, x, out);                                                              \
+        else hipLaunchKernelGGL((k_rg_products<NX, 4, 4>), grid, block, 0, s, T, d, ws, p, ws.er, a.dx_in, a.dx, x, \
+                                out);                                                                               \
+    } while (0)
+    if (a.x_bf16) GO(1);
+    else GO(3);
+#undef GO
     if (ws.S > 1) {
         const int64_t n4 = (int64_t)kE * d / 4;
         hipLaunchKernelGGL(k_rg_sum, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, n4, ws.S,
