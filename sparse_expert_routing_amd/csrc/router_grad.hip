@@ -264,22 +264,24 @@ __device__ __forceinline__ void dx_block(int T, int d, const RgWs &ws, const int
 #pragma unroll
     for (int j = 0; j < NJ; ++j) ec[j] = ws.ec[min(n0 + 32 * j + (lane & 31), d - 1)];
     all_landed();
-    // LDS: row 32 j + lane % 32 of term m at + 16 KB j + 64 KB m, piece 2 ks + g by one xor
+    // LDS: row 32 j + lane % 32 of a term at + 16 KB j, piece 2 ks + g by one xor
     const uint32_t row_off = (uint32_t)piece512(lane & 31, g);
-    f16x8 a[2][2][4];  // quarter of K (even, odd), term, step
-    auto load = [&](int ch, int q, f16x8 (&v)[2][4]) {
-        const uint16_t *p = ws.dlh + (int64_t)ch * 2 * 32 * kE + q * 4 * 512 + 8 * lane;
+    // a part of K: two steps of 16; buffer, term, step
+    constexpr int kParts = 4, kSteps = 16 / kParts;
+    f16x8 a[2][2][kSteps];
+    auto load = [&](int ch, int p, f16x8 (&v)[2][kSteps]) {
+        const uint16_t *from = ws.dlh + (int64_t)ch * 2 * 32 * kE + p * kSteps * 512 + 8 * lane;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            v[0][s] = *reinterpret_cast<const f16x8 *>(p + s * 512);
-            v[1][s] = *reinterpret_cast<const f16x8 *>(p + 32 * kE + s * 512);
+        for (int s = 0; s < kSteps; ++s) {
+            v[0][s] = *reinterpret_cast<const f16x8 *>(from + s * 512);
+            v[1][s] = *reinterpret_cast<const f16x8 *>(from + 32 * kE + s * 512);
         }
     };
     f32x16 acc[NJ];
-    auto quarter = [&](int q, const f16x8 (&v)[2][4]) {
+    auto part = [&](int p, const f16x8 (&v)[2][kSteps]) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint16_t *h = sw + (row_off ^ (uint32_t)(16 * (4 * q + s))), *m = h + kDxN * kE;
+        for (int s = 0; s < kSteps; ++s) {
+            const uint16_t *h = sw + (row_off ^ (uint32_t)(16 * (kSteps * p + s))), *m = h + kDxN * kE;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 const f16x8 bh = *reinterpret_cast<const f16x8 *>(h + 32 * j * kE);
@@ -290,21 +292,23 @@ __device__ __forceinline__ void dx_block(int T, int d, const RgWs &ws, const int
             }
         }
     };
-    // Stores count as loads in flight do, in order: two quarters of the next chunk are asked for
-    // ahead of a chunk's stores, so nothing waits for the stores but what comes a quarter later.
+    // A part is asked for two parts ahead of its use, the next chunk's first two ahead of a
+    // chunk's stores: stores count as loads in flight do, in order, so nothing waits for them
+    // but what comes a part later.
     if (c0 + wave < c1) {
         load(c0 + wave, 0, a[0]);
         load(c0 + wave, 1, a[1]);
     }
     for (int ch = c0 + wave; ch < c1; ch += 8) {
+        const int next = min(ch + 8, c1 - 1);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[j] = f32x16{};
-        quarter(0, a[0]);
-        __builtin_amdgcn_sched_barrier(0);
-        load(ch, 2, a[0]);
-        quarter(1, a[1]);
-        __builtin_amdgcn_sched_barrier(0);
-        load(ch, 3, a[1]);
+#pragma unroll
+        for (int p = 0; p < kParts / 2; ++p) {
+            part(p, a[p & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            load(ch, p + 2, a[p & 1]);
+        }
         // lane: column n0 + 32 j + lane % 32, tokens t0 + 8 q + 4 g + r; what is added to the
         // sums is asked for here, half the products ahead of its use
         const int t0 = ch * 32 + 4 * g, n = n0 + (lane & 31);
@@ -329,12 +333,12 @@ __device__ __forceinline__ void dx_block(int T, int d, const RgWs &ws, const int
                 }
         }
         __builtin_amdgcn_sched_barrier(0);
-        quarter(2, a[0]);
-        __builtin_amdgcn_sched_barrier(0);
-        load(min(ch + 8, c1 - 1), 0, a[0]);
-        quarter(3, a[1]);
-        __builtin_amdgcn_sched_barrier(0);
-        load(min(ch + 8, c1 - 1), 1, a[1]);
+#pragma unroll
+        for (int p = kParts / 2; p < kParts; ++p) {
+            part(p, a[p & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            load(p + 2 < kParts ? ch : next, (p + 2) % kParts, a[p & 1]);
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -479,32 +483,35 @@ __device__ __forceinline__ void dw_block(int T, int d, const RgWs &ws, const uin
         }
 }
 
-// Both products in one launch, so that dx, which waits for memory, and dw, which
-// keeps the matrix cores busy, run side by side: workgroups in turns of eight (an
-// XCD each) as long as both have some left.
 struct RgGrid {
     int dx_split, dx_tiles, dw_split, dw_tiles;
 };
-template <int NX, int NJ, int NB>
-__global__ __launch_bounds__(512, 1) void k_rg_products(int T, int d, const RgWs ws, const RgGrid p,
-                                                        const int32_t *__restrict__ er, const float *dx_in, float *dx,
-                                                        const uint16_t *__restrict__ x, float *__restrict__ out) {
-    constexpr int kDwLds = dw_ring<NX>() * dw_stage<NX, NB>(), kDxLds = 2 * 32 * NJ * kE;
+
+// Large problems, one launch each (T = 16384, d = 7168: 438 us in all; both in one
+// launch, in turns or one behind the other, 434 to 526, dx with two workgroups of 64
+// columns on a CU 489).
+constexpr int kLargeNJ = 4, kLargeNB = 4;
+__global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, const RgGrid p,
+                                                  const int32_t *__restrict__ er, const float *dx_in, float *dx) {
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[2 * 32 * kLargeNJ * kE];
+    dx_block<kLargeNJ>(T, d, ws, er, dx_in, dx, smem, blockIdx.x % p.dx_split, p.dx_split, blockIdx.x / p.dx_split);
+}
+template <int NX>
+__global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, const RgGrid p,
+                                                  const uint16_t *__restrict__ x, float *__restrict__ out) {
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[dw_ring<NX>() * dw_stage<NX, kLargeNB>()];
+    dw_block<NX, kLargeNB>(T, d, ws, x, out, smem, blockIdx.x % p.dw_split, p.dw_split, blockIdx.x / p.dw_split);
+}
+// Small ones, both in one launch: the dx blocks first.
+template <int NX>
+__global__ __launch_bounds__(512, 1) void k_rg_small(int T, int d, const RgWs ws, const RgGrid p,
+                                                     const int32_t *__restrict__ er, const float *dx_in, float *dx,
+                                                     const uint16_t *__restrict__ x, float *__restrict__ out) {
+    constexpr int kDwLds = dw_ring<NX>() * dw_stage<NX, 1>(), kDxLds = 2 * 32 * kE;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[kDwLds > kDxLds ? kDwLds : kDxLds];
-    const int ndx = p.dx_split * p.dx_tiles, ndw = p.dw_split * p.dw_tiles;
-    const int b = blockIdx.x, turns = min(ndx, ndw) / 8;
-    int at;
-    bool is_dx;
-    if (b < 16 * turns) {
-        is_dx = ((b >> 3) & 1) == 0;
-        at = (b >> 4) * 8 + (b & 7);
-    } else {
-        at = b - 8 * turns;
-        is_dx = at < ndx;
-        if (!is_dx) at = b - ndx;
-    }
-    if (is_dx) dx_block<NJ>(T, d, ws, er, dx_in, dx, smem, at % p.dx_split, p.dx_split, at / p.dx_split);
-    else dw_block<NX, NB>(T, d, ws, x, out, smem, at % p.dw_split, p.dw_split, at / p.dw_split);
+    const int ndx = p.dx_split * p.dx_tiles, at = (int)blockIdx.x - ndx;
+    if (at < 0) dx_block<1>(T, d, ws, er, dx_in, dx, smem, blockIdx.x % p.dx_split, p.dx_split, blockIdx.x / p.dx_split);
+    else dw_block<NX, 1>(T, d, ws, x, out, smem, at % p.dw_split, p.dw_split, at / p.dw_split);
 }
 
 // dw = the S partial sums added in order, 4 values per thread.
@@ -532,15 +539,19 @@ hipError_t launch_router_grad(const RouterGradArgs &a, void *workspace, hipStrea
                        static_cast<const float *>(a.x_bf16 ? nullptr : a.x), ws);
     const Cut c = cut_of(T, d);
     const RgGrid p{c.dx_split, (d + c.dx_cols - 1) / c.dx_cols, c.dw_split, (d + c.dw_cols - 1) / c.dw_cols};
-    const dim3 grid((unsigned)(p.dx_split * p.dx_tiles + p.dw_split * p.dw_tiles)), block(512);
+    const int ndx = p.dx_split * p.dx_tiles, ndw = p.dw_split * p.dw_tiles;
+    const dim3 block(512);
     float *out = ws.S == 1 ? a.dw : ws.part;
     const uint16_t *x = a.x_bf16 ? static_cast<const uint16_t *>(a.x) : ws.xs;
-#define GO(NX)                                                                                                      \
-    do {                                                                                                            \
-        if (c.small) hipLaunchKernelGGL((k_rg_products<NX, 1, 1>), grid, block, 0, s, T, d, ws, p, ws.er, a.dx_in,  \
-                                        a.dx, x, out);                                                              \
-        else hipLaunchKernelGGL((k_rg_products<NX, 4, 4>), grid, block, 0, s, T, d, ws, p, ws.er, a.dx_in, a.dx, x, \
-                                out);                                                                               \
+#define GO(NX)                                                                                                     \
+    do {                                                                                                           \
+        if (c.small) {                                                                                             \
+            hipLaunchKernelGGL(k_rg_small<NX>, dim3(ndx + ndw), block, 0, s, T, d, ws, p, ws.er, a.dx_in, a.dx, x, \
+                               out);                                                                               \
+        } else {                                                                                                   \
+            hipLaunchKernelGGL(k_rg_dx, dim3(ndx), block, 0, s, T, d, ws, p, ws.er, a.dx_in, a.dx);                \
+            hipLaunchKernelGGL(k_rg_dw<NX>, dim3(ndw), block, 0, s, T, d, ws, p, x, out);                          \
+        }                                                                                                          \
     } while (0)
     if (a.x_bf16) GO(1);
     else GO(3);
