@@ -369,6 +369,90 @@ LaneMap lane_map(const SelectRule &r) {
 // alike, nothing rounded), fp32 logits, or the biased fp32 scores.
 enum { KEY_BF16 = 0, KEY_F32 = 1, KEY_SCORE = 2 };
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+    return __longlong_as_double((long long)dpp_u64<CTRL>((uint64_t)__double_as_longlong(v)));
+}
+
+// Lanes of the row with a larger v, or the same and a lower id.
+__device__ __forceinline__ int row_rank64(double v, int id) {
+    int n = 0;
+#define ROR(N)                                                       \
+    {                                                                \
+        const double o = dpp_f64<0x120 + N>(v);                      \
+        const int oid = (int)dpp_u32<0x120 + N>((uint32_t)id);       \
+        n += o > v || (o == v && oid < id);                          \
+    }
+    ROR(1) ROR(2) ROR(3) ROR(4) ROR(5) ROR(6) ROR(7) ROR(8) ROR(9) ROR(10) ROR(11) ROR(12) ROR(13) ROR(14) ROR(15)
+#undef ROR
+    return n;
+}
+
+__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
+
+// Whether this lane's group is among the best ones, by 64-bit scores.  cand: the
+// lane's experts that can be one of its group's two best; lq: its logits in LDS.
+__device__ __forceinline__ bool settle_groups(uint32_t cand, const float *lq, const float *__restrict__ bias, int e0,
+                                              const LaneMap &map, int group, bool top_two, int want) {
+    double d1 = -INFINITY, d2 = -INFINITY;
+    for (; cand; cand &= cand - 1) {
+        const int q = __ffs(cand) - 1;
+        double v = bias || top_two ? sigmoid64(lq[q]) : (double)lq[q];
+        if (bias) v += (double)bias[e0 + q];
+        d2 = fmax(d2, fmin(d1, v));
+        d1 = fmax(d1, v);
+    }
+#define STEP(C, LANES)                                           \
+    if (map.lanes >= LANES) {                                    \
+        const double o1 = dpp_f64<C>(d1), o2 = dpp_f64<C>(d2);   \
+        d2 = fmax(fmin(d1, o1), fmax(d2, o2));                   \
+        d1 = fmax(d1, o1);                                       \
+    }
+    STEP(0xB1, 2) STEP(0x4E, 4) STEP(0x141, 8) STEP(0x140, 16)
+#undef STEP
+    return row_rank64(top_two && map.per > 1 ? d1 + d2 : d1, group) < want;
+}
+
+// Which of the experts of a row that are near its border are chosen, by 64-bit
+// scores: `need` of them.  near: the lane's, bit q; list: 16 values and ids of the
+// row in LDS.  Returns them by bit q; of more than 16 none is settled (false).
+struct BorderList {
+    double v[16];
+    int32_t id[16];
+};
+__device__ __forceinline__ bool settle_border(uint32_t &near, int need, const float *lq, const float *__restrict__ bias,
+                                              int e0, BorderList *list) {
+    const int sub = threadIdx.x & 15, mine = __popc(near), all = (int)row_add((uint32_t)mine);
+    uint32_t pos = (uint32_t)mine;
+    pos += row_shr<1>(pos);
+    pos += row_shr<2>(pos);
+    pos += row_shr<4>(pos);
+    pos += row_shr<8>(pos);
+    pos -= (uint32_t)mine;
+    if (all <= 16) {
+        uint32_t at = pos;
+        for (uint32_t c = near; c; c &= c - 1, ++at) {
+            const int q = __ffs(c) - 1;
+            list->v[at] = bias ? sigmoid64(lq[q]) + (double)bias[e0 + q] : (double)lq[q];
+            list->id[at] = e0 + q;
+        }
+    }
+    wave_sync();
+    const bool on = all <= 16 && sub < all;
+    const int rank = row_rank64(on ? list->v[on ? sub : 0] : -INFINITY, on ? list->id[on ? sub : 0] : 1 << 20);
+    wave_sync();
+    if (on) list->id[sub] = rank < need;
+    wave_sync();
+    uint32_t out = 0;
+    if (all <= 16) {
+        uint32_t at = pos;
+        for (uint32_t c = near; c; c &= c - 1, ++at)
+            if (list->id[at]) out |= c & -c;
+    }
+    near = out;
+    return all <= 16;
+}
+
 // Sixteen lanes per token, four tokens per wave.  A lane holds up to Q neighbouring
 // experts of one group, each group has 1, 2, 4, 8 or 16 neighbouring lanes (LaneMap;
 // all experts are one group where none is closed).  Keys are 31-bit unsigned numbers (0: not an expert, or its group is
@@ -376,6 +460,10 @@ enum { KEY_BF16 = 0, KEY_F32 = 1, KEY_SCORE = 2 };
 // number is at least 2^31 for a key below m and less for the others, and the
 // largest difference is the answer: one subtraction and half a three-way maximum
 // per key and round, four exchanges, k + 1 rounds.
+//
+// A sigmoid's doubts are settled where they arise, by the 64-bit scores of the few
+// experts that they are about (settle_groups, settle_border); a softmax's, whose
+// 64-bit scores need the whole row, and rows with a NaN go to choose64.
 //
 // fp32 scores: exp2 and reciprocal are off by one unit each, the exponent's
 // rounding moves a sigmoid by at most s (1 - s) |l| 2^-24 < 2^-26, a softmax by p x
@@ -393,6 +481,7 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
     constexpr int QS = Q / 4;  // experts per lane in the 64-bit code
     __shared__ __attribute__((aligned(16))) float sc[4][64 * Q];  // the scores; 64-bit ones in the 64-bit code
     __shared__ uint8_t open64[4][64 * QS];
+    __shared__ BorderList lists[4][4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane & 15;
     const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
     if (t0 >= T) return;
@@ -448,8 +537,8 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
     if (r.topk_group < r.n_group) {
         uint32_t g;
         const bool rounded = KEY == KEY_SCORE || r.top_two;
+        float a1 = -INFINITY, a2 = -INFINITY;
         if (r.top_two) {
-            float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
                 const float v = KEY == KEY_SCORE ? b[q] : q < n ? s[q] : -INFINITY;
@@ -464,9 +553,9 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
     }
             STEP(0xB1, 2) STEP(0x4E, 4) STEP(0x141, 8) STEP(0x140, 16)
 #undef STEP
-            if (map.per == 1) a2 = 0.f;
-            doubt |= group < map.groups && a1 + a2 != a1 + a2;
-            g = group < map.groups ? key31(a1 + a2) : 0;
+            const float sum = map.per == 1 ? a1 : a1 + a2;
+            doubt |= group < map.groups && sum != sum;
+            g = group < map.groups ? key31(sum) : 0;
         } else {
             g = key[0];
 #pragma unroll
@@ -477,13 +566,31 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
 #undef STEP
         }
         const int want = r.topk_group * map.lanes;
-        const bool is_open = row_rank(g) < want;
+        bool is_open = row_rank(g) < want;
         // equal groups at the border open together
-        doubt |= row_add(is_open ? 1u : 0u) != (uint32_t)want;
+        bool unsure = row_add(is_open ? 1u : 0u) != (uint32_t)want;
         if (rounded) {
             const uint32_t lo = row_min(is_open ? g : 0x7fffffffu), hi = row_max(is_open ? 0u : g);
             const float x = from_key31(lo), y = hi ? from_key31(hi) : -INFINITY;
-            doubt |= !(x - y > 2.f * (near + 4.76837158203125e-7f * fabsf(x)));
+            unsure |= !(x - y > 2.f * (near + 4.76837158203125e-7f * fabsf(x)));
+        }
+        if (r.softmax) {
+            doubt |= unsure;
+        } else if (__ballot(unsure)) {
+            // those that fp32 leaves among their group's two best, or its best
+            uint32_t cand = 0;
+            const float lo = r.top_two && map.per > 1 ? a2 : from_key31(g);
+            const float from = lo - 2.f * (near + 4.76837158203125e-7f * fabsf(lo));
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                sc[wave][lane * Q + q] = l[q];
+                const float v = KEY == KEY_SCORE ? b[q] : r.top_two ? s[q] : l[q];
+                if (unsure && q < n && !(v < from)) cand |= 1u << q;
+            }
+            wave_sync();
+            const bool settled = settle_groups(cand, &sc[wave][lane * Q], bias, e0, map, group, r.top_two, want);
+            is_open = unsure ? settled : is_open;
+            wave_sync();
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) key[q] = is_open ? key[q] : 0;
@@ -500,16 +607,61 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
         // none below: nothing (0) from here on
         at = d >= 0x80000000u ? at + d : 0;
     }
-    if (KEY == KEY_SCORE) {
-        const float x = from_key31(kth), y = at ? from_key31(at) : -INFINITY;
-        doubt |= !(x - y > near + 4.76837158203125e-7f * fabsf(x));
-    }
     // bit Q - 1 - q: expert e0 + q is chosen
     uint32_t chosen = 0;
 #pragma unroll
     for (int q = 0; q < Q; ++q) chosen = __builtin_amdgcn_alignbit(chosen, (kth - 1u) - key[q], 31);
+    bool unsure = row_add(__popc(chosen)) != (uint32_t)r.k || kth <= 1u || kth >= 0x80000000u;
+    if (KEY == KEY_SCORE) {
+        const float x = from_key31(kth), y = at ? from_key31(at) : -INFINITY;
+        unsure |= !(x - y > near + 4.76837158203125e-7f * fabsf(x));
+    }
+    if (r.softmax && KEY == KEY_SCORE) {
+        doubt |= unsure;
+    } else if (__ballot(unsure)) {
+        // the k-th largest again, equal keys counted one by one
+        uint32_t kk = 0x80000000u, seen = 0;
+        for (int i = 0; i < r.k; ++i) {
+            uint32_t d = key[0] - kk, same = 0;
+#pragma unroll
+            for (int q = 1; q < Q; ++q) d = max(d, key[q] - kk);
+            d = row_max(d);
+            const uint32_t below = d >= 0x80000000u ? kk + d : 0;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) same += key[q] == below;
+            same = row_add(same);
+            if (seen < (uint32_t)r.k && below) {
+                kk = below;
+                seen += same;
+            }
+        }
+        const bool found = seen >= (uint32_t)r.k && kk != 0x80000000u;
+        // above it by more than the error: chosen; within it: settled by 64-bit scores
+        uint32_t hi = kk, lo = kk;
+        if (KEY == KEY_SCORE) {
+            const float x = from_key31(kk), tol = near + 4.76837158203125e-7f * fabsf(x);
+            hi = key31(x + tol);
+            lo = key31(x - tol);
+        }
+        uint32_t sure = 0, border = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (unsure) sc[wave][lane * Q + q] = l[q];
+            sure |= key[q] > hi ? 1u << q : 0;
+            border |= key[q] <= hi && key[q] >= lo && key[q] != 0 ? 1u << q : 0;
+        }
+        if (!unsure || !found) border = 0;
+        wave_sync();
+        const int need = r.k - (int)row_add(__popc(sure));
+        const bool settled = settle_border(border, need, &sc[wave][lane * Q], KEY == KEY_SCORE ? bias : nullptr, e0,
+                                           &lists[wave][lane >> 4]);
+        if (unsure) {
+            chosen = __brev(sure | border) >> (32 - Q);
+            doubt |= !settled || !found || row_add(__popc(chosen)) != (uint32_t)r.k;
+        }
+        wave_sync();
+    }
     const uint32_t count = __popc(chosen);
-    doubt |= row_add(count) != (uint32_t)r.k || kth <= 1u || kth >= 0x80000000u;
 
     // the chosen scores' sum; a softmax's that underflows next to the row's largest is left to
     // the 64-bit code's way, which is relative to the largest chosen
