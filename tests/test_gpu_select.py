@@ -137,6 +137,26 @@ def test_select_near_the_border(score, groups, biased):
     np.testing.assert_allclose(f64(w), plain64.weights(l.double().numpy(), got, score, True, 1.0), rtol=rtol(l, E))
 
 
+@pytest.mark.parametrize("E,k,G,KG,gs", [(256, 8, 1, 1, "max"), (256, 8, 8, 4, "top2"), (150, 6, 3, 2, "max"),
+                                         (165, 9, 5, 2, "top2"), (496, 12, 16, 5, "top2"), (500, 8, 2, 1, "top2"),
+                                         (16, 5, 16, 7, "top2"), (64, 64, 4, 4, "max"), (510, 3, 3, 1, "max"),
+                                         (600, 8, 4, 3, "max"), (68, 7, 17, 5, "top2")], ids=str)
+@pytest.mark.parametrize("std", [1.0, 1e-2, 1e-4])
+def test_select_crowded_scores(E, k, G, KG, gs, std):
+    """The narrower the scores, the more tokens have a border that only 64 bits decide, of experts and of groups."""
+    T = 300
+    say(f"[select] crowded E={E} k={k} groups {KG} of {G} {gs} std={std}")
+    for dtype in ("f32", "bf16"):
+        l = logits_of(T, E, dtype, E + k, std=std)
+        bias = 0.05 * std * torch.randn(E, generator=torch.Generator().manual_seed(k))
+        for b in (bias, torch.zeros(E), None):
+            _, idx, w = run_select(l.cuda(), b.cuda() if b is not None else None, k=k, n_group=G, topk_group=KG,
+                                   group_score=gs)
+            ri, rw = plain64.select(f64(l), f64(b) if b is not None else None, k, "sigmoid", G, KG, gs)
+            assert np.array_equal(idx.cpu().numpy(), ri), (dtype, b is None)
+            np.testing.assert_allclose(f64(w), rw, rtol=rtol(l, E))
+
+
 def test_select_special_rows():
     """Masked logits (-inf, the type's lowest), NaN, infinities: ids stay distinct and in range, as documented."""
     E, k = 256, 8
