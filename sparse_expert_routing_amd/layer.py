@@ -1,4 +1,5 @@
-"""A DeepSeekMoE layer on one GPU: device buffers plus the five C-ABI calls.
+"""A DeepSeekMoE layer on one GPU: device buffers plus the C-ABI calls of a forward
+(five of them), and of a training step.
 
 torch is used for device memory and the stream only; each step of the layer
 runs in the HIP kernels behind include/moe.h.
@@ -23,13 +24,22 @@ def _dev(a, device):
 
 class MoeLayer:
     """Weights and scratch of one layer; ``forward`` runs route -> dispatch ->
-    expert FFN -> combine, ``update_bias`` the sign step, ``step`` both."""
+    expert FFN -> combine, ``update_bias`` the sign step, ``step`` both.
 
-    def __init__(self, T, d, I, act, wt, wr, experts: dict, shared: dict, E=256, k=8, device="cuda"):
+    router: how the experts are chosen, where not by moe_route's rule: the keywords of
+    ``selection`` (score, n_group, topk_group, group_score, renorm, scale).  The forward
+    then computes the logits (kept in ``logits``) and chooses from them.
+
+    A training step is ``forward``, ``checkpoint`` (what the backward needs of it, in 8
+    bits or as it is) and ``backward``; with a router also ``balance_loss``.  The routing
+    of the last forward is what they go by."""
+
+    def __init__(self, T, d, I, act, wt, wr, experts: dict, shared: dict, E=256, k=8, device="cuda", router=None):
         self.T, self.d, self.I, self.E, self.k = T, d, I, E, k
         self.act, self.wt = act, wt
         self.device = torch.device(device)
         self.desc = _lib.desc(T, d, E, k, I, act, wt)
+        self.sel = _lib.selection(T, E, k, **router) if router is not None else None
         self.wr = _dev(wr, self.device)
         self.ex = {n: (_dev(a, self.device) if a is not None else None) for n, a in experts.items()}
         self.sh = {n: (_dev(a, self.device) if a is not None else None) for n, a in shared.items()}
@@ -48,10 +58,11 @@ class MoeLayer:
         self.offsets = torch.empty(E + 1, **i32)
         self.row_src = torch.empty(A, **i32)
         self.row_of = torch.empty(A, **i32)
+        self.logits = torch.empty((T, E), dtype=torch.float32, device=dev) if self.sel is not None else None
         self.x_perm = self.x_perm_scale = None  # allocated on first use of the materialised dispatch
         self.y_perm = torch.empty((A, d), dtype=torch.float32 if self.wt == "f32" else torch.int16, device=dev)
         self.y = torch.empty((T, d), dtype=torch.float32, device=dev)
-        ws = max(_lib.workspace_bytes(self.desc, s) for s in (0, 1, 2, 3))
+        ws = max(_lib.workspace_bytes(self.desc, s) for s in (0, 1, 2, 3, _lib.MOE_WS_ROUTER_LOGITS))
         self.ws = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
 
     def ensure_x_perm(self):
@@ -67,7 +78,13 @@ class MoeLayer:
         materialises x_perm and moe_expert_ffn consumes it.  Both give the
         same y bit for bit."""
         D = self.desc
-        _lib.moe_route(D, x, self.wr, bias, self.idx, self.w, self.gap if gap else None, self.ws, stream)
+        if self.sel is None:
+            _lib.moe_route(D, x, self.wr, bias, self.idx, self.w, self.gap if gap else None, self.ws, stream)
+        else:
+            if gap:
+                raise ValueError("the gap is moe_route's: a layer with a router has none")
+            _lib.moe_router_logits(D, x, self.wr, self.logits, self.ws, stream)
+            _lib.moe_select(self.sel, self.logits, bias, self.idx, self.w, stream)
         if gather_in_gemm:
             _lib.moe_dispatch(D, self.idx, x, self.counts, self.offsets, self.row_src, self.row_of, None, None,
                               self.ws, stream)
@@ -81,6 +98,61 @@ class MoeLayer:
                                 stream)
         _lib.moe_combine(D, x, self.sh_w, self.y_perm, self.row_of, self.w, self.y, self.ws, stream)
         return self.y
+
+    def checkpoint(self, x, fmt="e4m3", stream=None):
+        """What the backward needs of the last forward: x and the routed outputs, in 8 bits ("e4m3" or "i8", half
+        the memory of "bf16", which keeps them as they are, the outputs until the next forward)."""
+        kept = []
+        for t in (x, self.y_perm):
+            if fmt == "bf16":
+                kept.append((t, None, fmt))
+                continue
+            codes = torch.empty(t.shape, dtype=torch.uint8, device=t.device)
+            scales = torch.empty((t.shape[0], (t.shape[1] + 127) // 128), dtype=torch.uint8, device=t.device)
+            _lib.moe_checkpoint_pack(t, codes, scales, fmt, stream)
+            kept.append((codes, scales, fmt))
+        return tuple(kept)
+
+    def balance_loss(self, seq_offsets, alpha, stream=None):
+        """The last forward's sequence-wise balance loss [n_seq] and the loads [n_seq, E] that its gradient needs."""
+        if self.sel is None:
+            raise ValueError("the balance loss needs a layer with a router: the logits are not kept without one")
+        n = seq_offsets.numel() - 1
+        loss = torch.empty(max(n, 0), dtype=torch.float32, device=self.device)
+        load = torch.empty((max(n, 0), self.E), dtype=torch.float32, device=self.device)
+        ws = torch.empty(max(_lib.balance_workspace_bytes(self.sel, n), 1), dtype=torch.uint8, device=self.device)
+        _lib.moe_balance_loss(self.sel, self.logits, self.idx, seq_offsets, alpha, loss, load, ws, stream)
+        return loss, load
+
+    def backward(self, x, kept, dy, seq_offsets=None, load=None, dloss=None, alpha=0.0, stream=None) -> dict:
+        """Gradients of the last forward's output (dy [T, d] fp32), as moe_backward names them, from what checkpoint()
+        kept; x is read where there is a router, by its projection's gradient.  With a router, dloss [n_seq] adds the
+        gradient of balance_loss(seq_offsets, alpha)."""
+        D, f32 = self.desc, dict(dtype=torch.float32, device=self.device)
+        T, d, I, E, k = self.T, self.d, self.I, self.E, self.k
+        if self.sel is None and dloss is not None:
+            raise ValueError("the balance loss needs a layer with a router")
+        if dloss is None:
+            seq_offsets = load = None
+        grads = {n: torch.empty(s, **f32) for n, s in (
+            ("dx", (T, d)), ("dw_gate", (E, I, d)), ("dw_up", (E, I, d)), ("dw_down", (E, d, I)), ("ds_gate", (I, d)),
+            ("ds_up", (I, d)), ("ds_down", (d, I)), ("dg", (T, k)))}
+        fused = self.sel is None
+        if fused:
+            grads["dw_router"] = torch.empty((E, d), **f32)
+        xs, ys = (_lib.saved(*part) for part in kept)
+        ws = torch.empty(_lib.workspace_bytes(D, _lib.MOE_WS_BACKWARD_SAVED), dtype=torch.uint8, device=self.device)
+        _lib.moe_backward_saved(D, xs, self.wr if fused else None, self.idx if fused else None, self.w, self.offsets,
+                                self.row_src, self.row_of, self.ex_w, self.sh_w, ys, dy, grads, ws, stream)
+        if not fused:
+            dlogits = torch.empty((T, E), **f32)
+            _lib.moe_select_backward(self.sel, self.logits, self.idx, grads["dg"], dlogits, seq_offsets, load, dloss, alpha,
+                                     stream)
+            grads["dw_router"] = torch.empty((E, d), **f32)
+            ws = torch.empty(_lib.workspace_bytes(D, _lib.MOE_WS_ROUTER_GRAD), dtype=torch.uint8, device=self.device)
+            _lib.moe_router_logits_backward(D, x, self.wr, dlogits, grads["dx"], grads["dx"], grads["dw_router"], ws,
+                                            stream)
+        return grads
 
     def update_bias(self, bias, gamma=1e-3, stream=None):
         _lib.moe_bias_update(self.desc, self.counts, gamma, bias, stream)
@@ -124,10 +196,10 @@ def load_bias(path, device="cuda") -> torch.Tensor:
     return torch.from_numpy(b).to(device)
 
 
-def layer_from_inputs(inp: dict, device="cuda") -> MoeLayer:
+def layer_from_inputs(inp: dict, device="cuda", router=None) -> MoeLayer:
     """Build a layer from a synth.make_inputs() dict (weights uploaded once)."""
     c = inp["cfg"]
-    return MoeLayer(c.T, c.d, c.I, c.act, c.wt, inp["wr"], inp["experts"], inp["shared"], c.E, c.k, device)
+    return MoeLayer(c.T, c.d, c.I, c.act, c.wt, inp["wr"], inp["experts"], inp["shared"], c.E, c.k, device, router)
 
 
 def upload(a, device="cuda"):
