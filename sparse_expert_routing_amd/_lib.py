@@ -221,8 +221,10 @@ def selection(T, E, k, score="sigmoid", n_group=1, topk_group=1, group_score="to
 
 
 def saved(data, scales=None, fmt="bf16") -> Saved:
-    """A saved activation (moe_saved_t): bf16 values, or 8-bit codes and their tiles' scales."""
-    return Saved(data.data_ptr(), scales.data_ptr() if scales is not None else None, SAVED_FORMATS[fmt])
+    """A saved activation (moe_saved_t): bf16 values, or 8-bit codes and their tiles' scales, which it keeps alive."""
+    s = Saved(data.data_ptr(), scales.data_ptr() if scales is not None else None, SAVED_FORMATS[fmt])
+    s.tensors = (data, scales)
+    return s
 
 
 def balance_workspace_bytes(sel: Select, n_seq: int) -> int:
@@ -254,7 +256,7 @@ class _Call:
     def __init__(self, fn):
         if _torch is None:
             _bind_torch()
-        self.fn, self.index, self.elsewhere = fn, -1, None
+        self.fn, self.index, self.elsewhere = fn, -2, None  # (-1 is the CPU)
 
     def refuse(self, what):
         raise MoeError(self.fn, MOE_EINVAL, "MOE_EINVAL: " + what)
@@ -271,7 +273,7 @@ class _Call:
             self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
         if not t.is_contiguous():
             self.refuse(f"{name} is not contiguous")
-        if t.get_device() != self.index or not t.is_cuda:
+        if t.get_device() != self.index:
             self.on(name, t)
         return t.data_ptr()
 
@@ -288,9 +290,20 @@ class _Call:
             ld = max(ld, shape[1])
         if (shape[1] > 1 and step != 1) or ld < shape[1]:
             self.refuse(f"{name} has strides {tuple(t.stride())}: its rows have to be contiguous and apart")
-        if t.get_device() != self.index or not t.is_cuda:
+        if t.get_device() != self.index:
             self.on(name, t)
         return t.data_ptr(), ld
+
+    def saved(self, name, s, rows, cols):
+        """A saved activation of that shape (its tensors are looked at where saved() made it)."""
+        if s is None:
+            self.refuse(f"{name} is missing")
+        data, scales = getattr(s, "tensors", (None, None))
+        if data is not None:
+            plain = s.format == MOE_SAVED_BF16
+            self.ptr(f"{name}'s values" if plain else f"{name}'s codes", data, MOE_BF16 if plain else "byte", (rows, cols))
+            self.ptr(f"{name}'s scales", scales, MOE_E4M3, (rows, (cols + 127) // 128), plain)
+        return ctypes.byref(s)
 
     def on(self, name, t):
         if self.index < 0 and t.is_cuda:
@@ -304,7 +317,7 @@ class _Call:
             return None, 0
         if not t.is_contiguous():
             self.refuse("the workspace is not contiguous")
-        if t.get_device() != self.index or not t.is_cuda:
+        if t.get_device() != self.index:
             self.on("the workspace", t)
         return t.data_ptr(), t.numel() * t.element_size()
 
@@ -422,7 +435,7 @@ def moe_checkpoint_unpack(codes, scales, fmt, dst, stream=None):
 def moe_combine_backward(ds, dy, y_perm: Saved, row_of, weights, dy_perm, dg, stream=None):
     """The combine's gradient from saved routed outputs: dy_perm [T*k, d] bf16 and dg [T, k]."""
     c = _Call("moe_combine_backward")
-    args = (c.ptr("dy", dy, MOE_F32, (ds.T, ds.d)), ctypes.byref(y_perm), c.ptr("row_of", row_of, "i32", (ds.T * ds.k,)),
+    args = (c.ptr("dy", dy, MOE_F32, (ds.T, ds.d)), c.saved("y_perm", y_perm, ds.T * ds.k, ds.d), c.ptr("row_of", row_of, "i32", (ds.T * ds.k,)),
             c.ptr("weights", weights, MOE_F32, (ds.T, ds.k)), c.ptr("dy_perm", dy_perm, MOE_BF16, (ds.T * ds.k, ds.d)),
             c.ptr("dg", dg, MOE_F32, (ds.T, ds.k)))
     c.run(load().moe_combine_backward, ctypes.byref(ds), *args, stream=stream)
@@ -435,11 +448,11 @@ def moe_backward_saved(ds, x: Saved, w_router, idx, weights, offsets, row_src, r
     c = _Call("moe_backward_saved")
     A, T, d, E, I = ds.T * ds.k, ds.T, ds.d, ds.E, ds.I
     own = w_router is None
-    head = (ctypes.byref(x), c.ptr("w_router", w_router, MOE_F32, (E, d), True),
+    head = (c.saved("x", x, T, d), c.ptr("w_router", w_router, MOE_F32, (E, d), True),
             c.ptr("idx", idx, "i32", (T, ds.k), own), c.ptr("weights", weights, MOE_F32, (T, ds.k)),
             c.ptr("offsets", offsets, "i32", (E + 1,)), c.ptr("row_src", row_src, "i32", (A,)),
-            c.ptr("row_of", row_of, "i32", (A,)), ctypes.byref(experts), ctypes.byref(shared), ctypes.byref(y_perm),
-            c.ptr("dy", dy, MOE_F32, (T, d)))
+            c.ptr("row_of", row_of, "i32", (A,)), ctypes.byref(experts), ctypes.byref(shared),
+            c.saved("y_perm", y_perm, A, d), c.ptr("dy", dy, MOE_F32, (T, d)))
     out = [c.ptr(n, grads.get(n), MOE_F32, s, n == "dg" or (n == "dw_router" and own))
            for n, s in (("dx", (T, d)), ("dw_router", (E, d)), ("dw_gate", (E, I, d)), ("dw_up", (E, I, d)),
                         ("dw_down", (E, d, I)), ("ds_gate", (I, d)), ("ds_up", (I, d)), ("ds_down", (d, I)),

@@ -267,7 +267,7 @@ __device__ __forceinline__ void dx_block(int T, int d, const RgWs &ws, const int
     // LDS: row 32 j + lane % 32 of a term at + 16 KB j, piece 2 ks + g by one xor
     const uint32_t row_off = (uint32_t)piece512(lane & 31, g);
     // a part of K: two steps of 16; buffer, term, step
-    constexpr int kParts = 4, kSteps = 16 / kParts;
+    constexpr int kParts = 8, kSteps = 16 / kParts;
     f16x8 a[2][2][kSteps];
     auto load = [&](int ch, int p, f16x8 (&v)[2][kSteps]) {
         const uint16_t *from = ws.dlh + (int64_t)ch * 2 * 32 * kE + p * kSteps * 512 + 8 * lane;
@@ -278,17 +278,34 @@ __device__ __forceinline__ void dx_block(int T, int d, const RgWs &ws, const int
         }
     };
     f32x16 acc[NJ];
+    // w's fragments of a step are read from LDS during the step before: step, block, term
+    f16x8 w[2][NJ][2];
+    auto fetch = [&](int step, f16x8 (&v)[NJ][2]) {
+        const uint16_t *h = sw + (row_off ^ (uint32_t)(16 * step));
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            v[j][0] = *reinterpret_cast<const f16x8 *>(h + 32 * j * kE);
+            v[j][1] = *reinterpret_cast<const f16x8 *>(h + (kDxN + 32 * j) * kE);
+        }
+    };
     auto part = [&](int p, const f16x8 (&v)[2][kSteps]) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const uint16_t *h = sw + (row_off ^ (uint32_t)(16 * (kSteps * p + s))), *m = h + kDxN * kE;
+            const int step = kSteps * p + s;
+            fetch((step + 1) & 15, w[(step + 1) & 1]);
+            const f16x8(&b)[NJ][2] = w[step & 1];
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const f16x8 bh = *reinterpret_cast<const f16x8 *>(h + 32 * j * kE);
-                const f16x8 bm = *reinterpret_cast<const f16x8 *>(m + 32 * j * kE);
-                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[1][s], bh, acc[j], 0, 0, 0);
-                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0][s], bm, acc[j], 0, 0, 0);
-                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0][s], bh, acc[j], 0, 0, 0);
+            for (int j = 0; j < NJ; ++j) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[1][s], b[j][0], acc[j], 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0][s], b[j][1], acc[j], 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0][s], b[j][0], acc[j], 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {  // two LDS reads among three products
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
             }
         }
     };
@@ -298,6 +315,7 @@ __device__ __forceinline__ void dx_block(int T, int d, const RgWs &ws, const int
     if (c0 + wave < c1) {
         load(c0 + wave, 0, a[0]);
         load(c0 + wave, 1, a[1]);
+        fetch(0, w[0]);
     }
     for (int ch = c0 + wave; ch < c1; ch += 8) {
         const int next = min(ch + 8, c1 - 1);

@@ -663,8 +663,8 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
     }
     const uint32_t count = __popc(chosen);
 
-    // the chosen scores' sum; a softmax's that underflows next to the row's largest is left to
-    // the 64-bit code's way, which is relative to the largest chosen
+    // the chosen scores' sum; one that underflows is left to the 64-bit code's way: a softmax's
+    // there is relative to the largest chosen, a sigmoid's keeps fp32's subnormals
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -672,7 +672,7 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
         sc[wave][lane * Q + q] = s[q];
     }
     sum = row_sum(sum);
-    doubt |= r.softmax && r.renorm && !(sum > 1e-30f);
+    doubt |= r.renorm && !(sum > 1e-30f);
     if (!r.renorm) sum = 1.f;
     uint32_t pos = count;
     pos += row_shr<1>(pos);

@@ -188,3 +188,21 @@ def test_binding_checks_come_in_front_of_the_device():
     s = _lib.selection(4, 16, 2)
     assert "is on meta" in refused(_lib.moe_select, s, torch.zeros(4, 16, **m), None, torch.zeros(4, 2, dtype=torch.int32, **m),
                                    torch.zeros(4, 2, **m))
+
+
+def test_binding_checks_saved_activations():
+    ds = good_desc(T=4)
+    dy, row_of, w = torch.zeros(4, 256), torch.zeros(32, dtype=torch.int32), torch.zeros(4, 8)
+    out, dg = torch.zeros(32, 256, dtype=torch.bfloat16), torch.zeros(4, 8)
+    q, s = torch.zeros(32, 256, dtype=torch.uint8), torch.zeros(32, 2, dtype=torch.uint8)
+
+    def why(saved):
+        return refused(_lib.moe_combine_backward, ds, dy, saved, row_of, w, out, dg)
+
+    assert "is on cpu" in why(_lib.saved(q, s, "e4m3"))
+    assert "missing" in why(None)
+    assert "codes has shape" in why(_lib.saved(q[:8], s, "i8"))
+    assert "scales has shape" in why(_lib.saved(q, s[:, :1].contiguous(), "i8"))
+    assert "scales is missing" in why(_lib.saved(q, None, "i8"))
+    assert "values has type" in why(_lib.saved(q))
+    assert "values has shape" in why(_lib.saved(out[:, :128].contiguous()))
