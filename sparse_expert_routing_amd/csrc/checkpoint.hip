@@ -270,6 +270,10 @@ struct Saved8 {
     }
 };
 
+// Bound by memory: T = 16384, d = 7168 from e4m3 674 us, 4.9 TB/s (one wave per token
+// 702); T = 2048, d = 2048 from int8 21 us (one wave and a row's load at a time 37,
+// stores through the caches 26).
+//
 // W waves per token, each on every W-th run of 512 columns.  A row_of entry outside
 // [0, T*8) is a choice that was not dispatched: it has no row to write and its
 // gradient is 0.

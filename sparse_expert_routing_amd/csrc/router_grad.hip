@@ -127,7 +127,7 @@ RgWs carve(char *base, int T, int d, bool x_bf16) {
     return w;
 }
 
-// The operands' terms in one launch.  Workgroups [0, nw): 64 columns of w each;
+// The operands' terms in one launch.  Workgroups [0, nw): 16 columns of w each;
 // [nw, nw + nt): 32 rows of dl each; the rest, for an fp32 x: 1024 of its values.
 __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, const float *__restrict__ w,
                                                   const float *__restrict__ dl, const float *__restrict__ x, RgWs ws) {
@@ -135,23 +135,24 @@ __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, 
     __shared__ int row_exp[32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if ((int)blockIdx.x < nw) {
-        // thread: column n, experts 64 wave .. +63
-        const int n = blockIdx.x * 64 + lane;
-        float v[64];
+        // thread: column n, experts 16 part .. +15
+        const int col = tid & 15, part = tid >> 4, n = blockIdx.x * 16 + col;
+        float v[16];
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            v[i] = w[(int64_t)(wave * 64 + i) * d + n];
+        for (int i = 0; i < 16; ++i) {
+            v[i] = w[(int64_t)(part * 16 + i) * d + n];
             m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
         }
         uint32_t *most = reinterpret_cast<uint32_t *>(&tile[0][0]);
         most[tid] = m;
         __syncthreads();
-        m = max(max(most[lane], most[64 + lane]), max(most[128 + lane], most[192 + lane]));
-        const int e = scale_exp(m);
-        if (wave == 0) ws.ec[n] = -e;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int i = 0; i < 16; ++i) m = max(m, most[16 * i + col]);
+        const int e = scale_exp(m);
+        if (part == 0) ws.ec[n] = -e;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
             i32x4 hi, mid;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, 
                 hi[i] = (int)(h0 | (h1 << 16));
                 mid[i] = (int)(m0 | (m1 << 16));
             }
-            uint16_t *o = ws.wh + (int64_t)n * kE + wave * 64 + 8 * c;
+            uint16_t *o = ws.wh + (int64_t)n * kE + part * 16 + 8 * c;
             *reinterpret_cast<i32x4 *>(o) = hi;
             *reinterpret_cast<i32x4 *>(o + (int64_t)d * kE) = mid;
         }
@@ -505,9 +506,11 @@ struct RgGrid {
     int dx_split, dx_tiles, dw_split, dw_tiles;
 };
 
-// Large problems, one launch each (T = 16384, d = 7168: 438 us in all; both in one
-// launch, in turns or one behind the other, 434 to 526, dx with two workgroups of 64
-// columns on a CU 489).
+// Large problems, one launch each.  T = 16384, d = 7168: dx 237 us, 4.0 TB/s of what
+// it reads and writes; dw 156 us, the matrix cores 60% busy at 2.05 GHz; 422 us in
+// all with the terms and the sum (fp32 library products: 1247).  On one card each:
+// both in one launch 548 against 522 us, dx with two workgroups of 64 columns on a CU
+// 551 against 506.
 constexpr int kLargeNJ = 4, kLargeNB = 4;
 __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, const RgGrid p,
                                                   const int32_t *__restrict__ er, const float *dx_in, float *dx) {
@@ -520,7 +523,8 @@ __global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, c
     __shared__ __attribute__((aligned(1024))) uint16_t smem[dw_ring<NX>() * dw_stage<NX, kLargeNB>()];
     dw_block<NX, kLargeNB>(T, d, ws, x, out, smem, blockIdx.x % p.dw_split, p.dw_split, blockIdx.x / p.dw_split);
 }
-// Small ones, both in one launch: the dx blocks first.
+// Small ones, both in one launch, the dx blocks first: T = 301, d = 896 8 us, where
+// the large tiles in two launches took 31.
 template <int NX>
 __global__ __launch_bounds__(512, 1) void k_rg_small(int T, int d, const RgWs ws, const RgGrid p,
                                                      const int32_t *__restrict__ er, const float *dx_in, float *dx,
@@ -550,7 +554,7 @@ size_t router_grad_ws_bytes(int T, int d, bool x_bf16) { return carve(nullptr, T
 hipError_t launch_router_grad(const RouterGradArgs &a, void *workspace, hipStream_t s) {
     const int T = a.T, d = a.d;
     const RgWs ws = carve(static_cast<char *>(workspace), T, d, a.x_bf16);
-    const int nw = d / 64, nt = ws.Tp / 32;
+    const int nw = d / 16, nt = ws.Tp / 32;
     const int64_t nx = a.x_bf16 ? 0 : ((int64_t)T * d / 4 + 255) / 256;
     if (nw + nt + nx > INT32_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_rg_split, dim3((unsigned)(nw + nt + nx)), dim3(256), 0, s, T, d, nw, nt, a.w, a.dlogits,
