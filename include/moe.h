@@ -332,6 +332,7 @@ moe_status_t moe_backward(const moe_desc_t *desc, const void *x, const float *w_
  *   logits   [T, E]  fp32 out
  *   workspace >= moe_workspace_bytes(desc, MOE_WS_ROUTER_LOGITS) bytes of
  *            device memory (0 for fp32 activations; NULL allowed then)
+ * x and logits are 16-byte aligned.
  */
 moe_status_t moe_router_logits(const moe_desc_t *desc, const void *x, const float *w_router, float *logits,
                                void *workspace, size_t ws_bytes, void *stream);
@@ -422,7 +423,7 @@ moe_status_t moe_select_backward(const moe_select_t *sel, const void *logits, in
  *   seq_offsets [n_seq + 1] int32 on the device, ascending, in [0, T]; empty
  *               sequences are allowed (loss 0, load 0)
  *   loss [n_seq], load [n_seq, E] fp32 out
- *   workspace >= moe_balance_workspace_bytes(sel, n_seq) bytes
+ *   workspace >= moe_balance_workspace_bytes(sel, n_seq) bytes, 16-byte aligned
  * Of the rule T, E, k, score and logits are read.  Deterministic.
  */
 moe_status_t moe_balance_loss(const moe_select_t *sel, const void *logits, int64_t ld, const int32_t *idx,
@@ -490,6 +491,7 @@ moe_status_t moe_combine_backward(const moe_desc_t *desc, const float *dy, const
  * it is moe_backward, bit for bit.
  *   workspace >= moe_workspace_bytes(desc, MOE_WS_BACKWARD_SAVED) bytes:
  *   moe_backward's and one bf16 [T, d].
+ * The saved data, dy and the workspace are 16-byte aligned.
  */
 moe_status_t moe_backward_saved(const moe_desc_t *desc, const moe_saved_t *x, const float *w_router,
                                 const int32_t *idx, const float *weights, const int32_t *offsets,

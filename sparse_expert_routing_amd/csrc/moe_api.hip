@@ -443,6 +443,7 @@ moe_status_t moe_backward_saved(const moe_desc_t *d, const moe_saved_t *x, const
         !ffn_weights_ok(shared, d->wt))
         return MOE_EINVAL;
     if (w_router ? (!dw_router || !idx) : (dw_router || !dg)) return MOE_EINVAL;
+    if (!aligned16(dy) || !aligned16(workspace)) return MOE_EINVAL;
     if (!workspace || ws_bytes < backward_saved_ws(d)) return MOE_EWORKSPACE;
     return backward_of(d, x, w_router, idx, weights, offsets, row_src, row_of, experts, shared, y_perm, dy, dx, dw_router,
                        dw_gate, dw_up, dw_down, ds_gate, ds_up, ds_down, dg, workspace, saved_x_bytes(d), stream);
@@ -481,7 +482,7 @@ moe_status_t moe_router_logits(const moe_desc_t *d, const void *x, const float *
                                void *workspace, size_t ws_bytes, void *stream) {
     moe_status_t st = check_desc(d);
     if (st != MOE_OK) return st;
-    if (!x || !w_router || !logits) return MOE_EINVAL;
+    if (!x || !w_router || !logits || !aligned16(x) || !aligned16(logits)) return MOE_EINVAL;
     const size_t need = route_ws(d);
     if (need && (!workspace || ws_bytes < need)) return MOE_EWORKSPACE;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -534,6 +535,7 @@ moe_status_t moe_balance_loss(const moe_select_t *sel, const void *logits, int64
     moe_status_t st = check_select(sel);
     if (st != MOE_OK) return st;
     if (!logits || !idx || !seq_offsets || !loss || !load || n_seq <= 0 || ld < sel->E) return MOE_EINVAL;
+    if (!aligned16(workspace)) return MOE_EINVAL;
     if (!workspace || ws_bytes < moe_balance_workspace_bytes(sel, n_seq)) return MOE_EWORKSPACE;
     const moe::BalanceArgs a{rule_of(sel), sel->T, sel->logits == MOE_BF16, logits, ld, idx, seq_offsets, n_seq, alpha,
                              loss, load};

@@ -102,15 +102,15 @@ class MoeLayer:
     def checkpoint(self, x, fmt="e4m3", stream=None):
         """What the backward needs of the last forward: x and the routed outputs, in 8 bits ("e4m3" or "i8", half
         the memory of "bf16", which keeps them as they are, the outputs until the next forward)."""
+        if fmt == "bf16":
+            return (x, None, fmt), (self.y_perm, None, fmt)
         kept = []
-        for t in (x, self.y_perm):
-            if fmt == "bf16":
-                kept.append((t, None, fmt))
-                continue
-            codes = torch.empty(t.shape, dtype=torch.uint8, device=t.device)
-            scales = torch.empty((t.shape[0], (t.shape[1] + 127) // 128), dtype=torch.uint8, device=t.device)
-            _lib.moe_checkpoint_pack(t, codes, scales, fmt, stream)
-            kept.append((codes, scales, fmt))
+        with torch.cuda.stream(stream):
+            for t in (x, self.y_perm):
+                codes = torch.empty(t.shape, dtype=torch.uint8, device=t.device)
+                scales = torch.empty((t.shape[0], (t.shape[1] + 127) // 128), dtype=torch.uint8, device=t.device)
+                _lib.moe_checkpoint_pack(t, codes, scales, fmt)
+                kept.append((codes, scales, fmt))
         return tuple(kept)
 
     def balance_loss(self, seq_offsets, alpha, stream=None):
@@ -118,40 +118,42 @@ class MoeLayer:
         if self.sel is None:
             raise ValueError("the balance loss needs a layer with a router: the logits are not kept without one")
         n = seq_offsets.numel() - 1
-        loss = torch.empty(max(n, 0), dtype=torch.float32, device=self.device)
-        load = torch.empty((max(n, 0), self.E), dtype=torch.float32, device=self.device)
-        ws = torch.empty(max(_lib.balance_workspace_bytes(self.sel, n), 1), dtype=torch.uint8, device=self.device)
-        _lib.moe_balance_loss(self.sel, self.logits, self.idx, seq_offsets, alpha, loss, load, ws, stream)
+        with torch.cuda.stream(stream):
+            loss = torch.empty(max(n, 0), dtype=torch.float32, device=self.device)
+            load = torch.empty((max(n, 0), self.E), dtype=torch.float32, device=self.device)
+            ws = torch.empty(max(_lib.balance_workspace_bytes(self.sel, n), 1), dtype=torch.uint8, device=self.device)
+            _lib.moe_balance_loss(self.sel, self.logits, self.idx, seq_offsets, alpha, loss, load, ws)
         return loss, load
 
     def backward(self, x, kept, dy, seq_offsets=None, load=None, dloss=None, alpha=0.0, stream=None) -> dict:
         """Gradients of the last forward's output (dy [T, d] fp32), as moe_backward names them, from what checkpoint()
         kept; x is read where there is a router, by its projection's gradient.  With a router, dloss [n_seq] adds the
         gradient of balance_loss(seq_offsets, alpha)."""
-        D, f32 = self.desc, dict(dtype=torch.float32, device=self.device)
-        T, d, I, E, k = self.T, self.d, self.I, self.E, self.k
         if self.sel is None and dloss is not None:
             raise ValueError("the balance loss needs a layer with a router")
         if dloss is None:
             seq_offsets = load = None
+        # results and workspaces are the stream's own: freed here, they serve only what follows on it
+        with torch.cuda.stream(stream):
+            return self._backward(x, kept, dy, seq_offsets, load, dloss, alpha)
+
+    def _backward(self, x, kept, dy, seq_offsets, load, dloss, alpha) -> dict:
+        D, f32 = self.desc, dict(dtype=torch.float32, device=self.device)
+        T, d, I, E, k = self.T, self.d, self.I, self.E, self.k
         grads = {n: torch.empty(s, **f32) for n, s in (
             ("dx", (T, d)), ("dw_gate", (E, I, d)), ("dw_up", (E, I, d)), ("dw_down", (E, d, I)), ("ds_gate", (I, d)),
-            ("ds_up", (I, d)), ("ds_down", (d, I)), ("dg", (T, k)))}
-        fused = self.sel is None
-        if fused:
-            grads["dw_router"] = torch.empty((E, d), **f32)
+            ("ds_up", (I, d)), ("ds_down", (d, I)), ("dg", (T, k)), ("dw_router", (E, d)))}
         xs, ys = (_lib.saved(*part) for part in kept)
         ws = torch.empty(_lib.workspace_bytes(D, _lib.MOE_WS_BACKWARD_SAVED), dtype=torch.uint8, device=self.device)
-        _lib.moe_backward_saved(D, xs, self.wr if fused else None, self.idx if fused else None, self.w, self.offsets,
-                                self.row_src, self.row_of, self.ex_w, self.sh_w, ys, dy, grads, ws, stream)
-        if not fused:
-            dlogits = torch.empty((T, E), **f32)
-            _lib.moe_select_backward(self.sel, self.logits, self.idx, grads["dg"], dlogits, seq_offsets, load, dloss, alpha,
-                                     stream)
-            grads["dw_router"] = torch.empty((E, d), **f32)
-            ws = torch.empty(_lib.workspace_bytes(D, _lib.MOE_WS_ROUTER_GRAD), dtype=torch.uint8, device=self.device)
-            _lib.moe_router_logits_backward(D, x, self.wr, dlogits, grads["dx"], grads["dx"], grads["dw_router"], ws,
-                                            stream)
+        experts = (self.w, self.offsets, self.row_src, self.row_of, self.ex_w, self.sh_w, ys, dy)
+        if self.sel is None:
+            _lib.moe_backward_saved(D, xs, self.wr, self.idx, *experts, grads, ws)
+            return grads
+        _lib.moe_backward_saved(D, xs, None, None, *experts, {n: g for n, g in grads.items() if n != "dw_router"}, ws)
+        dlogits = torch.empty((T, E), **f32)
+        _lib.moe_select_backward(self.sel, self.logits, self.idx, grads["dg"], dlogits, seq_offsets, load, dloss, alpha)
+        ws = torch.empty(_lib.workspace_bytes(D, _lib.MOE_WS_ROUTER_GRAD), dtype=torch.uint8, device=self.device)
+        _lib.moe_router_logits_backward(D, x, self.wr, dlogits, grads["dx"], grads["dx"], grads["dw_router"], ws)
         return grads
 
     def update_bias(self, bias, gamma=1e-3, stream=None):

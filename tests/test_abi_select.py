@@ -59,6 +59,7 @@ def test_null_rule_and_pointers():
     for args, st in (((P, 256, P, P, 0, 0.1, P, P, P, need), EINVAL), ((P, 256, P, None, 5, 0.1, P, P, P, need), EINVAL),
                      ((P, 256, None, P, 5, 0.1, P, P, P, need), EINVAL), ((P, 256, P, P, 5, 0.1, None, P, P, need), EINVAL),
                      ((P, 256, P, P, 5, 0.1, P, None, P, need), EINVAL), ((P, 200, P, P, 5, 0.1, P, P, P, need), EINVAL),
+                     ((P, 256, P, P, 5, 0.1, P, P, P + 4, need), EINVAL),
                      ((P, 256, P, P, 5, 0.1, P, P, P, need - 1), EWORKSPACE),
                      ((P, 256, P, P, 5, 0.1, P, P, None, need), EWORKSPACE)):
         assert L.moe_balance_loss(r, *args, None) == st
@@ -128,6 +129,7 @@ def test_backward_saved_refusals():
     assert need >= _lib.workspace_bytes(ds, _lib.MOE_WS_BACKWARD) + 64 * 256 * 2
     assert call_backward_saved(ds, ok, ok, nb=need - 1) == EWORKSPACE
     assert call_backward_saved(ds, ok, ok, ws=None) == EWORKSPACE
+    assert call_backward_saved(ds, ok, ok, ws=P + 8) == EINVAL
     assert call_backward_saved(good_desc(act="f32", wt="f32"), ok, ok) == ENOTSUP
     assert _lib.workspace_bytes(good_desc(act="f32", wt="f32"), _lib.MOE_WS_BACKWARD_SAVED) == 0
 
@@ -140,6 +142,8 @@ def test_router_logits_refusals():
         a = [None if i == j else P for j in range(3)]
         assert L.moe_router_logits(ctypes.byref(ds), *a, P, need, None) == EINVAL
     assert L.moe_router_logits(ctypes.byref(ds), P, P, P, P, need - 1, None) == EWORKSPACE
+    assert L.moe_router_logits(ctypes.byref(ds), P + 2, P, P, P, need, None) == EINVAL
+    assert L.moe_router_logits(ctypes.byref(ds), P, P, P + 4, P, need, None) == EINVAL
     need = _lib.workspace_bytes(ds, _lib.MOE_WS_ROUTER_GRAD)
     for i in (0, 1, 2, 4, 5):
         a = [None if i == j else P for j in range(6)]

@@ -175,6 +175,24 @@ def test_combine_backward(T, d, fmt):
     assert torch.equal(dyp, want)
 
 
+def test_combine_backward_past_32_bit_offsets():
+    T, d = 270_001, 1024  # 2.2e9 routed values
+    say(f"[combine-grad] T={T} d={d}")
+    codes = torch.randint(0, 255, (T * 8, d), dtype=torch.uint8, device="cuda")
+    scales = torch.full((T * 8, d // 128), 120, dtype=torch.uint8, device="cuda")
+    row_of = torch.arange(T * 8 - 1, -1, -1, dtype=torch.int32, device="cuda")  # the first token's rows last
+    w, dy = torch.rand(T, 8, device="cuda"), torch.randn(T, d, device="cuda")
+    dyp = torch.empty(T * 8, d, dtype=torch.bfloat16, device="cuda")
+    dg = torch.empty(T, 8, device="cuda")
+    _lib.moe_combine_backward(_lib.desc(T, d, 256, 8, 128), dy, _lib.saved(codes, scales, "i8"), row_of, w, dyp, dg)
+    for t in (0, 1, T // 2, T - 1):
+        rows = row_of[8 * t:8 * t + 8].long()
+        y = codes[rows].view(torch.int8).double() * 2.0**-7
+        prod = y * dy[t].double()
+        assert ((dg[t].double() - prod.sum(1)).abs() <= (d / 64 + 8) * plain64.EPS32 * prod.abs().sum(1)).all()
+        assert torch.equal(dyp[rows], (w[t][:, None] * dy[t]).bfloat16())
+
+
 # ---------------------------------------------------------------- the layer's backward
 
 def layer_case(wt, T=600, d=256, I=256, seed=3):

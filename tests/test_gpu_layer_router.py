@@ -129,6 +129,35 @@ def test_layer_without_a_router_trains_by_moe_backward():
         layer.backward(x, layer.checkpoint(x, "bf16"), dy, dloss=torch.ones(1, device="cuda"))
 
 
+def test_training_step_on_a_side_stream():
+    """A step whose calls are given a stream other than the current one, while the current one allocates and
+    overwrites: everything of it belongs to that stream."""
+    say("[layer-router] side stream")
+    _, layer, x, bias = case("bf16", router=ROUTERS["grouped sigmoid"])
+    off = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    dy = torch.randn(layer.T, layer.d, generator=torch.Generator().manual_seed(1)).cuda()
+    dloss = torch.ones(2, device="cuda")
+
+    def step(stream):
+        layer.forward(x, bias, stream=stream)
+        loss, load = layer.balance_loss(off, 0.01, stream=stream)
+        kept = layer.checkpoint(x, "i8", stream=stream)
+        if stream is not None:
+            junk = [torch.full((1 << 22,), 7.0, device="cuda") for _ in range(8)]
+        g = layer.backward(x, kept, dy, off, load, dloss, 0.01, stream=stream)
+        if stream is not None:
+            junk += [torch.full((1 << 24,), 7.0, device="cuda") for _ in range(8)]
+        return dict(loss=loss, load=load, **g)
+
+    ref = {n: t.clone() for n, t in step(None).items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(ref[n], got[n]) for n in ref)
+
+
 def test_training_step_replays_from_a_graph():
     """One captured step (forward, loss, checkpoint, backward, bias step) replayed on new inputs beside eager work,
     each replay against the eager step on a layer of its own."""

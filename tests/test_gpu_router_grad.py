@@ -74,6 +74,27 @@ def test_router_grad(T, d, act, sparse):
     assert torch.equal(run(x, w, dl, dx3, dx3, act), dw) and torch.equal(dx3, dx[:T])
 
 
+def test_router_grad_past_32_bit_offsets():
+    T, d = 2_100_003, 1024  # 2.15e9 values of x
+    say(f"[router-grad] T={T} d={d}")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(T, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = torch.randn(256, d, device="cuda", generator=g) * d**-0.5
+    dl = torch.randn(T, 256, device="cuda", generator=g)
+    dx = torch.empty(T, d, device="cuda")
+    dw = run(x, w, dl, None, dx, "bf16")
+    for part in (slice(0, 300), slice(T - 300, T)):
+        L, W = dl[part].double(), w.double()
+        assert ((dx[part].double() - L @ W).abs() <= 260 * plain64.EPS32 * (L.abs() @ W.abs()) + 1e-9).all()
+    ref, size = 0, 0
+    for xs, ls in zip(x.split(1 << 18), dl.split(1 << 18)):
+        ref = ref + ls.double().t() @ xs.double()
+        size = size + ls.double().abs().t() @ xs.double().abs()
+    # a split's 4096-odd products at a time in fp32, the splits' sums behind one another
+    assert ((dw.double() - ref).abs() <= (T / 16 + 300) * plain64.EPS32 * size).all()
+    assert float((dw.double() - ref).norm()) <= 1e-5 * float(ref.norm())
+
+
 def test_router_grad_zeros_and_extremes():
     """Rows and columns of zeros, tiny and large magnitudes."""
     T, d = 200, 256

@@ -197,6 +197,53 @@ def test_select_special_rows():
                     assert (got[0] == 0).all() and (got[8] == 0).all()  # no score at all: weight 0
 
 
+def test_select_past_32_bit_offsets():
+    """More than 2^31 logits: the last tokens as a call of their own has them, their gradient and their loss too."""
+    T, E, k, n = 8_400_003, 256, 2, 500
+    say(f"[select] T={T} E={E}")
+    l = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_()
+    bias = (0.1 * torch.rand(E, generator=torch.Generator().manual_seed(1)) - 0.05).cuda()
+    sel, idx, w = run_select(l, bias, k=k)
+    few, fi, fw = run_select(l[-n:].clone(), bias, k=k)
+    assert torch.equal(idx[-n:], fi) and torch.equal(w[-n:], fw)
+    ri, _ = plain64.select(f64(l[-n:]), f64(bias), k, "sigmoid")
+    assert np.array_equal(fi.cpu().numpy(), ri)
+    off = torch.tensor([T - n, T], dtype=torch.int32, device="cuda")
+    loss, load = torch.empty(1, device="cuda"), torch.empty(1, E, device="cuda")
+    ws = torch.empty(_lib.balance_workspace_bytes(sel, 1), dtype=torch.uint8, device="cuda")
+    _lib.moe_balance_loss(sel, l, idx, off, 0.5, loss, load, ws)
+    rl, rf = plain64.balance(f64(l[-n:]), ri, [0, n], 0.5, "sigmoid")
+    np.testing.assert_allclose(f64(loss), rl, rtol=1e-5)
+    np.testing.assert_allclose(f64(load), rf, rtol=1e-6)
+    dw = torch.randn(T, k, device="cuda")
+    out = torch.empty(T, E, device="cuda")
+    _lib.moe_select_backward(sel, l, idx, dw, out, off, load, torch.ones(1, device="cuda"), 0.5)
+    ref = plain64.select_grad(f64(l[-n:]), ri, f64(dw[-n:]), "sigmoid", True, 1.0, [0, n], f64(load), np.ones(1), 0.5)
+    assert np.abs(f64(out[-n:]) - ref).max() <= 2 * rtol(l[-n:], E) * float(dw[-n:].abs().max() + 1)
+
+
+def test_select_unaligned_inputs():
+    """Logits, bias and gradients that begin at any element."""
+    T, E, k = 70, 128, 6
+    say("[select] unaligned")
+    for dtype in ("f32", "bf16"):
+        flat = logits_of(1, T * E + 1, dtype, 5).cuda().view(-1)
+        b = (0.1 * torch.rand(E + 1, generator=torch.Generator().manual_seed(2))).cuda()[1:]
+        l = flat[1:].view(T, E)
+        _, idx, w = run_select(l, b, k=k, n_group=4, topk_group=2)
+        ri, rw = plain64.select(f64(l), f64(b), k, "sigmoid", 4, 2)
+        assert np.array_equal(idx.cpu().numpy(), ri)
+        np.testing.assert_allclose(f64(w), rw, rtol=rtol(l, E))
+        sel = _lib.selection(T, E, k, logits=dtype)
+        out = torch.empty(T * E + 1, device="cuda")[1:].view(T, E)
+        dw = torch.randn(T * k + 1, device="cuda")[1:].view(T, k)
+        off = torch.tensor([0, 0, 50], dtype=torch.int32, device="cuda")[1:]
+        load = torch.rand(E + 1, device="cuda")[1:].view(1, E)
+        _lib.moe_select_backward(sel, l, idx, dw, out, off, load, torch.ones(1, device="cuda"), 0.1)
+        ref = plain64.select_grad(f64(l), ri, f64(dw), "sigmoid", True, 1.0, [0, 50], f64(load), np.ones(1), 0.1)
+        assert np.abs(f64(out) - ref).max() <= 2 * rtol(l, E) * float(dw.abs().max() + 1)
+
+
 def test_select_strided_rows_and_neighbours():
     T, E, k = 37, 200, 5
     say("[select] strided logits")
