@@ -122,10 +122,11 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
     return m;
 }
 
-// v of another lane of the row of 16.
+// v of another lane of the row of 16, for controls that have one for every lane
+// (no old value to keep: the move folds into the operation that uses it).
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
 // Partner exchanges that combine 2, 4, 8, 16 neighbouring lanes when applied in
 // this order (the mirrors meet lanes that already hold their half's result).
