@@ -264,8 +264,8 @@ __device__ __forceinline__ int row_rank(uint32_t v) {
     return n;
 }
 
-// 31-bit ordered key of a float (its last mantissa bit goes), 1 at least.
-__device__ __forceinline__ uint32_t key31(float v) { return (f32_order_key(v + 0.f) >> 1) | (v == -INFINITY); }
+// 31-bit ordered key of a number (its last mantissa bit goes), never 0.
+__device__ __forceinline__ uint32_t key31(float v) { return f32_order_key(v + 0.f) >> 1; }
 __device__ __forceinline__ float from_key31(uint32_t k) { return f32_from_order_key(k << 1); }
 
 __device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(1.4426950408889634f * v); }
@@ -453,7 +453,8 @@ __device__ __forceinline__ bool settle_border(uint32_t &near, int need, const fl
     return all <= 16;
 }
 
-// Sixteen lanes per token, four tokens per wave.  A lane holds up to Q neighbouring
+// Sixteen lanes per token, four tokens per wave (FULL: every lane has Q experts, in
+// whole vectors, and none is masked).  A lane holds up to Q neighbouring
 // experts of one group, each group has 1, 2, 4, 8 or 16 neighbouring lanes (LaneMap;
 // all experts are one group where none is closed).  Keys are 31-bit unsigned numbers (0: not an expert, or its group is
 // closed), so that with the largest key below m wanted, k - m as an unsigned
@@ -476,7 +477,7 @@ __device__ __forceinline__ bool settle_border(uint32_t &near, int need, const fl
 // per token takes 52), 32 tokens 6 us: bound by the instructions and latencies of
 // one round of waves, about 1000 instructions per four tokens.  Without the
 // settling of borders, its few 64-bit tokens made that 17 us.
-template <int Q, int KEY, bool BF16>
+template <int Q, int KEY, bool BF16, bool FULL>
 __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, bool vec, int T,
                                                      const void *__restrict__ logits, int64_t ld,
                                                      const float *__restrict__ bias, int32_t *__restrict__ idx,
@@ -491,14 +492,17 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
     const int64_t t = min(t0 + (lane >> 4), (int64_t)T - 1);
     const bool mine = t0 + (lane >> 4) < T;
     const int group = sub >> map.shift, e1 = (sub & (map.lanes - 1)) * map.run;  // in the group
-    const int e0 = group * map.per + e1, n = group < map.groups ? min(map.run, map.per - e1) : 0;
+    const int e0 = FULL ? sub * Q : group * map.per + e1;
+    const int n = FULL ? Q : group < map.groups ? min(map.run, map.per - e1) : 0;
     float l[Q], b[Q];
-    load_row<Q, BF16>(logits, t * ld, e0, n, vec, l);
-    if (KEY == KEY_SCORE) load_row<Q, false>(bias, 0, e0, n, vec, b);
-    // a NaN ranks behind every number: the 64-bit code's business
+    load_row<Q, BF16>(logits, t * ld, e0, n, FULL || vec, l);
+    if (KEY == KEY_SCORE) load_row<Q, false>(bias, 0, e0, n, FULL || vec, b);
+    // a NaN ranks behind every number: the 64-bit code's business (a biased score's is looked for below)
     bool doubt = false;
+    if (KEY != KEY_SCORE) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) doubt |= l[q] != l[q];
+        for (int q = 0; q < Q; ++q) doubt |= l[q] != l[q];
+    }
 
     float s[Q], total = 1.f, m = 0.f;
     if (r.softmax) {
@@ -1037,22 +1041,27 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
         const bool vec = map.per % Q == 0 && reinterpret_cast<uintptr_t>(a.logits) % step == 0 &&
                          a.ld * bytes % step == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
         if (vec) map.run = Q;
-#define FAST(QQ)                                                                                                     \
-    do {                                                                                                             \
-        if (a.bias && a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, true>), grid, block, 0, s, r, map,     \
-                                                 vec, a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                \
-        else if (a.bias) hipLaunchKernelGGL((k_select_fast<QQ, KEY_SCORE, false>), grid, block, 0, s, r, map, vec,   \
-                                            a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                          \
-        else if (a.bf16) hipLaunchKernelGGL((k_select_fast<QQ, KEY_BF16, true>), grid, block, 0, s, r, map, vec,     \
-                                            a.T, a.logits, a.ld, a.bias, a.idx, a.weights);                          \
-        else hipLaunchKernelGGL((k_select_fast<QQ, KEY_F32, false>), grid, block, 0, s, r, map, vec, a.T, a.logits, \
-                                a.ld, a.bias, a.idx, a.weights);                                                     \
+        const bool full = vec && r.E == 16 * Q;
+#define FAST_KEY(QQ, KEY, BF16)                                                                                     \
+    do {                                                                                                            \
+        if (full) hipLaunchKernelGGL((k_select_fast<QQ, KEY, BF16, true>), grid, block, 0, s, r, map, vec, a.T,     \
+                                     a.logits, a.ld, a.bias, a.idx, a.weights);                                     \
+        else hipLaunchKernelGGL((k_select_fast<QQ, KEY, BF16, false>), grid, block, 0, s, r, map, vec, a.T,         \
+                                a.logits, a.ld, a.bias, a.idx, a.weights);                                          \
+    } while (0)
+#define FAST(QQ)                                                    \
+    do {                                                            \
+        if (a.bias && a.bf16) FAST_KEY(QQ, KEY_SCORE, true);        \
+        else if (a.bias) FAST_KEY(QQ, KEY_SCORE, false);            \
+        else if (a.bf16) FAST_KEY(QQ, KEY_BF16, true);              \
+        else FAST_KEY(QQ, KEY_F32, false);                          \
     } while (0)
         if (Q == 4) FAST(4);
         else if (Q == 8) FAST(8);
         else if (Q == 16) FAST(16);
         else FAST(32);
 #undef FAST
+#undef FAST_KEY
         return hipGetLastError();
     }
     const dim3 grid((unsigned)(((int64_t)a.T + 3) / 4));
