@@ -235,13 +235,15 @@ def _library():
     return load()
 
 
-_torch = None
+_torch = _raw_stream = _current_device = None
 _KINDS = {}
 
 
 def _bind_torch():
-    global _torch
+    global _torch, _raw_stream, _current_device
     import torch
+    # the current stream's handle and the current device without an object made for them
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     # the torch types a storage type travels in (bf16 also as its 16-bit patterns)
     _KINDS.update({MOE_F32: (torch.float32,), MOE_BF16: (torch.bfloat16, torch.int16), MOE_E4M3: (torch.uint8,),
                    "i32": (torch.int32,), "byte": (torch.uint8, torch.int8)})
@@ -324,17 +326,17 @@ class _Call:
     def run(self, call, *args, stream=None):
         if self.elsewhere is not None:
             self.refuse(self.elsewhere)
-        index, cuda = self.index, _torch.cuda
+        index = self.index
         if stream is None:
-            raw = _torch._C._cuda_getCurrentRawStream(index)
+            raw = _raw_stream(index)
         elif stream.device.index != index:
             self.refuse(f"the stream is on {stream.device}, not cuda:{index}")
         else:
             raw = stream.cuda_stream
-        if cuda.current_device() == index:
+        if _current_device() == index:
             st = call(*args, raw)
         else:
-            with cuda.device(index):
+            with _torch.cuda.device(index):
                 st = call(*args, raw)
         if st != MOE_OK:
             _check(self.fn, st)
