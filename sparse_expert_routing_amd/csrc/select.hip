@@ -921,6 +921,9 @@ __global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, in
     const int t = (int)min(max(c0, (int64_t)max(seq[s], 0)), (int64_t)T);
     const int end = (int)min(min(c0 + kBalanceTokens, (int64_t)max(seq[s + 1], 0)), (int64_t)T);
     if (t >= end) return;
+    // this thread's first choice, asked for ahead of the scores
+    const int64_t first = (int64_t)t * r.k + tid, behind = (int64_t)end * r.k;
+    const int mine = first < behind ? idx[first] : -1;
     for (int e = tid; e < 16 * Q; e += 512) hist[e] = 0;
     float sum[Q];
 #pragma unroll
@@ -952,7 +955,8 @@ __global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, in
         if (lane < 16) share[wave][spread(sub, q)] = sum[q];
     }
     __syncthreads();
-    for (int i = t * r.k + tid; i < end * r.k; i += 512) {
+    if (mine >= 0 && mine < r.E) atomicAdd(&hist[mine], 1);
+    for (int64_t i = first + 512; i < behind; i += 512) {
         const int e = idx[i];
         if (e >= 0 && e < r.E) atomicAdd(&hist[e], 1);
     }

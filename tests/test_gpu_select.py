@@ -432,6 +432,22 @@ def test_balance_loss_and_its_gradient(T, E, k, score, dtype, n, first, last):
     assert (out[outside.cuda()] == 0).all()
 
 
+def test_balance_loss_of_as_many_choices_as_there_may_be():
+    """T * k = 2^31 - 64, the most that is taken: every expert chosen by every token."""
+    E = k = 64
+    T = (1 << 25) - 1
+    say(f"[balance] T={T} k={k}")
+    l = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    idx = torch.arange(E, dtype=torch.int32, device="cuda").repeat(T, 1)
+    off = torch.tensor([0, 5, T - 3, T], dtype=torch.int32, device="cuda")
+    sel = _lib.selection(T, E, k, logits="bf16")
+    ws = torch.empty(_lib.balance_workspace_bytes(sel, 3), dtype=torch.uint8, device="cuda")
+    loss, load = torch.empty(3, device="cuda"), torch.empty(3, E, device="cuda")
+    _lib.moe_balance_loss(sel, l, idx, off, 0.25, loss, load, ws)
+    assert (load == 1).all()
+    np.testing.assert_allclose(f64(loss), 0.25, rtol=1e-6)
+
+
 def test_balance_loss_of_a_balanced_sequence_is_alpha():
     say("[balance] balanced")
     T, E, k = 64, 64, 4
