@@ -81,8 +81,10 @@ struct RgWs {
 };
 
 // How the two products are cut into workgroups.  Large problems: 128 columns per dx
-// block and 256 per dw block, about one of each per CU.  Where those are too few
-// to fill the card, 32 and 64.
+// block and 256 per dw block, about one of each per CU.  Below, 32 and 64, two
+// workgroups per CU: T = 2048, d = 4096 50 us instead of 64 (T = d = 4096, where the
+// large tiles begin: 82 and 89 with bf16 x, 140 and 132 with fp32 x; T = 16384,
+// d = 2048: 182 and 146).
 struct Cut {
     bool small;
     int dx_cols, dw_cols, dx_split, dw_split;
@@ -90,7 +92,7 @@ struct Cut {
 Cut cut_of(int T, int d) {
     Cut c{};
     const int rounds = (T + 255) / 256, stages = (T + kStageK - 1) / kStageK;
-    c.small = (int64_t)((d + 127) / 128) * rounds < 128;
+    c.small = (int64_t)((d + 127) / 128) * rounds < 512;
     c.dx_cols = c.small ? 32 : 128;
     c.dw_cols = c.small ? 64 : 256;
     const int dx_tiles = (d + c.dx_cols - 1) / c.dx_cols, dw_tiles = (d + c.dw_cols - 1) / c.dw_cols;
@@ -128,48 +130,46 @@ RgWs carve(char *base, int T, int d, bool x_bf16) {
 }
 
 // The operands' terms in one launch.  Workgroups [0, nw): 16 columns of w each;
-// [nw, nw + nt): 32 rows of dl each; the rest, for an fp32 x: 1024 of its values.
-__global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, const float *__restrict__ w,
+// [nw, nw + nt): 32 rows of dl each; the rest, for an fp32 x: 2048 of its values.
+// A thread's loads are all asked for before the first is used: at small sizes this
+// launch is one such round trip.
+__global__ __launch_bounds__(512) void k_rg_split(int T, int d, int nw, int nt, const float *__restrict__ w,
                                                   const float *__restrict__ dl, const float *__restrict__ x, RgWs ws) {
-    __shared__ float tile[32][kE + 4];
+    __shared__ __attribute__((aligned(16))) float tile[32][kE + 4];
     __shared__ int row_exp[32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if ((int)blockIdx.x < nw) {
-        // thread: column n, experts 16 part .. +15
+        // thread: column n, experts 8 part .. +7
         const int col = tid & 15, part = tid >> 4, n = blockIdx.x * 16 + col;
-        float v[16];
+        float v[8];
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[i] = w[(int64_t)(part * 16 + i) * d + n];
-            m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = w[(int64_t)(part * 8 + i) * d + n];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
         uint32_t *most = reinterpret_cast<uint32_t *>(&tile[0][0]);
         most[tid] = m;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = max(m, most[16 * i + col]);
+        for (int i = 0; i < 32; ++i) m = max(m, most[16 * i + col]);
         const int e = scale_exp(m);
         if (part == 0) ws.ec[n] = -e;
+        i32x4 hi, mid;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            i32x4 hi, mid;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t h0, m0, h1, m1;
-                split_f16(ldexpf(v[8 * c + 2 * i], e), h0, m0);
-                split_f16(ldexpf(v[8 * c + 2 * i + 1], e), h1, m1);
-                hi[i] = (int)(h0 | (h1 << 16));
-                mid[i] = (int)(m0 | (m1 << 16));
-            }
-            uint16_t *o = ws.wh + (int64_t)n * kE + part * 16 + 8 * c;
-            *reinterpret_cast<i32x4 *>(o) = hi;
-            *reinterpret_cast<i32x4 *>(o + (int64_t)d * kE) = mid;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h0, m0, h1, m1;
+            split_f16(ldexpf(v[2 * i], e), h0, m0);
+            split_f16(ldexpf(v[2 * i + 1], e), h1, m1);
+            hi[i] = (int)(h0 | (h1 << 16));
+            mid[i] = (int)(m0 | (m1 << 16));
         }
+        uint16_t *o = ws.wh + (int64_t)n * kE + part * 8;
+        *reinterpret_cast<i32x4 *>(o) = hi;
+        *reinterpret_cast<i32x4 *>(o + (int64_t)d * kE) = mid;
         return;
     }
     if ((int)blockIdx.x >= nw + nt) {
-        const int64_t at = ((int64_t)(blockIdx.x - nw - nt) * 256 + tid) * 4, n = (int64_t)T * d;
+        const int64_t at = ((int64_t)(blockIdx.x - nw - nt) * 512 + tid) * 4, n = (int64_t)T * d;
         if (at >= n) return;  // n is a multiple of 4
         const f32x4 v = *reinterpret_cast<const f32x4 *>(x + at);
         uint32_t t[4][3];
@@ -181,25 +181,30 @@ __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, 
         return;
     }
     const int t0 = (blockIdx.x - nw) * 32;
-    for (int r = wave; r < 32; r += 4) {  // a wave per row: 4 experts per lane
-        const int t = t0 + r;
-        f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (t < T) v = *reinterpret_cast<const f32x4 *>(dl + (int64_t)t * kE + 4 * lane);
-        *reinterpret_cast<f32x4 *>(&tile[r][4 * lane]) = v;
+    f32x4 v[4];  // wave: rows 4 wave .. +3; lane: 4 experts
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 4 * wave + i;
+        v[i] = t < T ? *reinterpret_cast<const f32x4 *>(dl + (int64_t)t * kE + 4 * lane) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * wave + i;
+        *reinterpret_cast<f32x4 *>(&tile[r][4 * lane]) = v[i];
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        for (int c = 0; c < 4; ++c) m = max(m, __float_as_uint(v[i][c]) & 0x7fffffffu);
         for (int s = 32; s >= 1; s >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, s, kWave));
         if (lane == 0) {
             row_exp[r] = scale_exp(m);
-            ws.er[t] = -row_exp[r];
+            ws.er[t0 + r] = -row_exp[r];
         }
     }
     __syncthreads();
     // thread: 8 experts of a row, the 16 bytes of one lane of a fragment
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int at = c * 256 + tid, m = at & 31, k = 8 * (at >> 5), e = row_exp[m];
+    for (int c = 0; c < 2; ++c) {
+        const int at = c * 512 + tid, m = at & 31, k = 8 * (at >> 5), e = row_exp[m];
         const f32x4 v0 = *reinterpret_cast<const f32x4 *>(&tile[m][k]);
         const f32x4 v1 = *reinterpret_cast<const f32x4 *>(&tile[m][k + 4]);
         i32x4 hi, mid;
@@ -215,22 +220,23 @@ __global__ __launch_bounds__(256) void k_rg_split(int T, int d, int nw, int nt, 
         *reinterpret_cast<i32x4 *>(o) = hi;
         *reinterpret_cast<i32x4 *>(o + 32 * kE) = mid;
     }
-    // thread: expert tid, its 32 tokens in a row
+    // thread: expert tid % 256, 16 of the tokens in a row
+    const int ex = tid & (kE - 1), half = tid >> 8;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2; ++c) {
         i32x4 o[3];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t a[3], b[3];
-            split_bf16(tile[8 * c + 2 * i][tid], a);
-            split_bf16(tile[8 * c + 2 * i + 1][tid], b);
+            split_bf16(tile[16 * half + 8 * c + 2 * i][ex], a);
+            split_bf16(tile[16 * half + 8 * c + 2 * i + 1][ex], b);
 #pragma unroll
             for (int j = 0; j < 3; ++j) o[j][i] = (int)(a[j] | (b[j] << 16));
         }
 #pragma unroll
         for (int j = 0; j < 3; ++j)
-            *reinterpret_cast<i32x4 *>(ws.dlt + ((int64_t)(t0 / kStageK + c / 2) * 3 + j) * kE * kStageK +
-                                       piece32(tid, c & 1)) = o[j];
+            *reinterpret_cast<i32x4 *>(ws.dlt + ((int64_t)(t0 / kStageK + half) * 3 + j) * kE * kStageK +
+                                       piece32(ex, c)) = o[j];
     }
 }
 
@@ -398,21 +404,22 @@ __device__ __forceinline__ void dma16_unseen(const void *src, const uint16_t *ld
 }
 
 // 256 experts x 64 NB columns per workgroup, 8 waves of 64 x 32 NB, stages of K = 16
-// in a ring of 5 (NB = 4, bf16 x: three terms of dl^T, 24 KB, and x, 8 KB: 160 KB),
-// four of them in flight.  x lies K-major and is read with transposing LDS reads:
+// in a ring (NB = 4, bf16 x: 5 of three terms of dl^T, 24 KB, and x, 8 KB: 160 KB),
+// all but one of them in flight.  x lies K-major and is read with transposing LDS reads:
 // within each 16 lanes, lane 4a + c receives element c of the 8 bytes that lanes a,
 // a+4, a+8, a+12 point at; its 16-byte piece c of row k sits at c ^ 4 (k % 4) (rows
 // of 512 bytes) or c ^ 2 (k % 4) (128 bytes, where two rows share the banks).
 template <int NX, int NB>
 constexpr int dw_stage() { return 3 * kE * kStageK + NX * kStageK * 64 * NB; }  // elements
-template <int NX>
-constexpr int dw_ring() { return NX == 1 ? 5 : 3; }
+// Stages in the ring: what one workgroup per CU has room for, or two (NB = 1).
+template <int NX, int NB>
+constexpr int dw_ring() { return NB == 1 ? (NX == 1 ? 3 : 2) : (NX == 1 ? 5 : 3); }
 template <int NX, int NB>
 __device__ __forceinline__ void dw_block(int T, int d, const RgWs &ws, const uint16_t *__restrict__ x,
                                          float *__restrict__ out, uint16_t *smem, int z, int S, int y) {
     constexpr int kDwN = 64 * NB, kPieces = kDwN / 8, kTurn = NB == 4 ? 4 : 2;
     constexpr int kA = 3 * kE * kStageK, kX = kStageK * kDwN;  // elements per stage
-    constexpr int kBuf = kA + NX * kX, kRing = dw_ring<NX>();
+    constexpr int kBuf = kA + NX * kX, kRing = dw_ring<NX, NB>();
     constexpr int kRowsPer = 64 / kPieces;                // rows of x per load instruction
     constexpr int kXWaves = kStageK / kRowsPer;           // waves that load x
     constexpr int kLoads = 3 + NX;                        // per wave and stage
@@ -474,11 +481,11 @@ __device__ __forceinline__ void dw_block(int T, int d, const RgWs &ws, const uin
     for (int i = 0; i < kRing - 1; ++i) issue(s0 + i, smem + i * kBuf);
     int at = 0, next = kRing - 1;
     for (int st = s0; st < s1; ++st) {
-        // all but the youngest kRing - 2 stages of this wave's loads have landed; behind the
-        // barrier every wave's, and the stage before is no longer read
+        // all but the youngest kRing - 2 stages of this wave's loads have landed and its LDS
+        // reads are done; behind the barrier every wave's, and the stage before is no longer read
         constexpr int kLeft = kLoads * (kRing - 2);
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        __builtin_amdgcn_s_waitcnt((kLeft & 15) | (7 << 4) | (15 << 8) | ((kLeft >> 4) << 14));
+        __builtin_amdgcn_s_waitcnt((kLeft & 15) | (7 << 4) | ((kLeft >> 4) << 14));
         __builtin_amdgcn_s_barrier();
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         issue(st + kRing - 1, smem + next * kBuf);
@@ -520,16 +527,17 @@ __global__ __launch_bounds__(512, 1) void k_rg_dx(int T, int d, const RgWs ws, c
 template <int NX>
 __global__ __launch_bounds__(512, 1) void k_rg_dw(int T, int d, const RgWs ws, const RgGrid p,
                                                   const uint16_t *__restrict__ x, float *__restrict__ out) {
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[dw_ring<NX>() * dw_stage<NX, kLargeNB>()];
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[dw_ring<NX, kLargeNB>() * dw_stage<NX, kLargeNB>()];
     dw_block<NX, kLargeNB>(T, d, ws, x, out, smem, blockIdx.x % p.dw_split, p.dw_split, blockIdx.x / p.dw_split);
 }
-// Small ones, both in one launch, the dx blocks first: T = 301, d = 896 8 us, where
-// the large tiles in two launches took 31.
+// Small ones, both in one launch, the dx blocks first, two workgroups per CU: T = 301,
+// d = 896 6.0 us, where the large tiles in two launches took 31; T = d = 2048 22.6 us
+// (one workgroup per CU 24.2), about 10 TB/s of terms read out of the L2s.
 template <int NX>
-__global__ __launch_bounds__(512, 1) void k_rg_small(int T, int d, const RgWs ws, const RgGrid p,
+__global__ __launch_bounds__(512, 4) void k_rg_small(int T, int d, const RgWs ws, const RgGrid p,
                                                      const int32_t *__restrict__ er, const float *dx_in, float *dx,
                                                      const uint16_t *__restrict__ x, float *__restrict__ out) {
-    constexpr int kDwLds = dw_ring<NX>() * dw_stage<NX, 1>(), kDxLds = 2 * 32 * kE;
+    constexpr int kDwLds = dw_ring<NX, 1>() * dw_stage<NX, 1>(), kDxLds = 2 * 32 * kE;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[kDwLds > kDxLds ? kDwLds : kDxLds];
     const int ndx = p.dx_split * p.dx_tiles, at = (int)blockIdx.x - ndx;
     if (at < 0) dx_block<1>(T, d, ws, er, dx_in, dx, smem, blockIdx.x % p.dx_split, p.dx_split, blockIdx.x / p.dx_split);
@@ -555,9 +563,9 @@ hipError_t launch_router_grad(const RouterGradArgs &a, void *workspace, hipStrea
     const int T = a.T, d = a.d;
     const RgWs ws = carve(static_cast<char *>(workspace), T, d, a.x_bf16);
     const int nw = d / 16, nt = ws.Tp / 32;
-    const int64_t nx = a.x_bf16 ? 0 : ((int64_t)T * d / 4 + 255) / 256;
+    const int64_t nx = a.x_bf16 ? 0 : ((int64_t)T * d / 4 + 511) / 512;
     if (nw + nt + nx > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_rg_split, dim3((unsigned)(nw + nt + nx)), dim3(256), 0, s, T, d, nw, nt, a.w, a.dlogits,
+    hipLaunchKernelGGL(k_rg_split, dim3((unsigned)(nw + nt + nx)), dim3(512), 0, s, T, d, nw, nt, a.w, a.dlogits,
                        static_cast<const float *>(a.x_bf16 ? nullptr : a.x), ws);
     const Cut c = cut_of(T, d);
     const RgGrid p{c.dx_split, (d + c.dx_cols - 1) / c.dx_cols, c.dw_split, (d + c.dw_cols - 1) / c.dw_cols};

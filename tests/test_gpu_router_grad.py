@@ -74,6 +74,17 @@ def test_router_grad(T, d, act, sparse):
     assert torch.equal(run(x, w, dl, dx3, dx3, act), dw) and torch.equal(dx3, dx[:T])
 
 
+@pytest.mark.parametrize("T,d,act", [(4099, 4096, "f32"), (4500, 4032, "f32"), (9001, 1920, "bf16"), (3900, 4096, "bf16")])
+def test_router_grad_about_the_large_tiles(T, d, act):
+    """The first sizes of the large tiles, ragged in both directions, and the last of the small ones."""
+    say(f"[router-grad] T={T} d={d} {act}")
+    x, w, dl, dx_in = inputs(T, d, act, T + d, False)
+    dx = torch.full((T + 1, d), -7.0, device="cuda")
+    dw = run(x, w, dl, dx_in, dx[:T], act)
+    check(x, w, dl, dx_in, dx[:T], dw)
+    assert (dx[T:] == -7).all()
+
+
 def test_router_grad_past_32_bit_offsets():
     T, d = 2_100_003, 1024  # 2.15e9 values of x
     say(f"[router-grad] T={T} d={d}")
