@@ -19,7 +19,8 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 size_t elem_bytes(int dt) { return dt == kF32 ? 4 : dt == kBF16 ? 2 : 1; }
 
 // Shape validation shared by every call.
-moe_status_t check_desc(const moe_desc_t *d) {
+// What holds for every entry; the combine's gradient, which no weights enter, asks no more.
+moe_status_t check_shape(const moe_desc_t *d) {
     if (d == nullptr) return MOE_EINVAL;
     if (d->T <= 0 || d->d <= 0 || d->E <= 0 || d->k <= 0 || d->I <= 0) return MOE_EINVAL;
     if (d->k > d->E) return MOE_EINVAL;
@@ -30,9 +31,14 @@ moe_status_t check_desc(const moe_desc_t *d) {
     if (!pair_ok) return MOE_ENOTSUP;
     if (d->E != 256 || d->k != 8) return MOE_ENOTSUP;
     if (d->d % 64 != 0 || d->I % 64 != 0) return MOE_ENOTSUP;
-    if (d->wt == MOE_BF16 && d->d % 128 != 0) return MOE_ENOTSUP;
     // 32-bit row indices and element offsets within one row block
     if ((long long)d->T * d->k >= (1LL << 31)) return MOE_ENOTSUP;
+    return MOE_OK;
+}
+moe_status_t check_desc(const moe_desc_t *d) {
+    const moe_status_t st = check_shape(d);
+    if (st != MOE_OK) return st;
+    if (d->wt == MOE_BF16 && d->d % 128 != 0) return MOE_ENOTSUP;
     return MOE_OK;
 }
 
@@ -451,7 +457,7 @@ moe_status_t moe_backward_saved(const moe_desc_t *d, const moe_saved_t *x, const
 
 moe_status_t moe_combine_backward(const moe_desc_t *d, const float *dy, const moe_saved_t *y_perm,
                                   const int32_t *row_of, const float *weights, void *dy_perm, float *dg, void *stream) {
-    moe_status_t st = check_desc(d);
+    moe_status_t st = check_shape(d);
     if (st != MOE_OK) return st;
     if (!dy || !row_of || !weights || !dy_perm || !dg || !saved_ok(y_perm)) return MOE_EINVAL;
     if (!aligned16(dy) || !aligned16(dy_perm)) return MOE_EINVAL;

@@ -175,6 +175,23 @@ def test_combine_backward(T, d, fmt):
     assert torch.equal(dyp, want)
 
 
+@pytest.mark.parametrize("T,d", [(3, 64), (1101, 320), (77, 2112)])
+@pytest.mark.parametrize("fmt", ["e4m3", "i8", "bf16"])
+def test_combine_backward_takes_half_a_tile_with_any_types(T, d, fmt):
+    """d of 64 more than a multiple of 128, which the products with bf16 weights refuse: as with fp32 ones."""
+    say(f"[combine-grad] T={T} d={d} {fmt}, both pairs of types")
+    s, _, row_of, w, dy = combine_inputs(T, d, fmt, T + d)
+    got = []
+    for types in ("f32", "bf16"):
+        dyp = torch.full((T * 8, d), -7.0, dtype=torch.bfloat16, device="cuda")
+        dg = torch.full((T, 8), -7.0, device="cuda")
+        _lib.moe_combine_backward(_lib.desc(T, d, 256, 8, 128, types, types), dy, _lib.saved(s[0], s[1], fmt), row_of, w,
+                                  dyp, dg)
+        got.append((dyp, dg))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert (got[1][1] != -7).all()
+
+
 def test_combine_backward_past_32_bit_offsets():
     T, d = 270_001, 1024  # 2.2e9 routed values
     say(f"[combine-grad] T={T} d={d}")
