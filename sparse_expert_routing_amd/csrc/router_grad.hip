@@ -102,7 +102,7 @@ Cut cut_of(int T, int d) {
     // dw: eight stages at least.  Neighbouring workgroups take different splits, so with a
     // multiple of 8 each XCD works on its own tokens and keeps their dl terms in its L2: worth
     // a sixteenth of the CUs (d = 2560, T = 12000: 24 splits 49 us, 25 52), not an eighth
-    // (T = 16384: d = 7168 9 splits 144 us, 8 153; d = 5120 12 splits 109, 8 143).
+    // (T = 16384: d = 7168 9 splits 148 us, 8 155; d = 5120 12 splits 109, 8 143).
     c.dw_split = 256 / dw_tiles;
     if (c.dw_split / 8 * 8 * 16 >= c.dw_split * 15) c.dw_split = c.dw_split / 8 * 8;
     const int most = (stages + 7) / 8;
@@ -516,7 +516,7 @@ struct RgGrid {
 };
 
 // Large problems, one launch each.  T = 16384, d = 7168: dx 235 us, 4.0 TB/s of what
-// it reads and writes; dw 144 us, the matrix cores 65% busy at 2.05 GHz; 420 us in
+// it reads and writes; dw 148 us, the matrix cores 67% busy at 2.0 GHz; 420 us in
 // all with the terms and the sum (fp32 library products: 1247).  On one card each:
 // both in one launch 548 against 522 us, dx with two workgroups of 64 columns on a CU
 // 551 against 506; dx's columns and tokens in even shares for all 256 CUs (224 have

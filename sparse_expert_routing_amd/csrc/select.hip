@@ -473,8 +473,8 @@ __device__ __forceinline__ bool settle_border(uint32_t &near, int need, const fl
 // are nearer than 2^-20 (sigmoid) or 2^-17 (softmax) plus 2^-21 of their size: twice
 // those errors with room.  That is also where equal keys end up.
 //
-// 8 of 256 experts in 8 groups, biased sigmoid: 16384 tokens 13 us (17.8 MB; the wave
-// per token takes 52), 32 tokens 6 us: bound by the instructions and latencies of
+// 8 of 256 experts in 8 groups, biased sigmoid: 16384 tokens 12 us (17.8 MB; the wave
+// per token takes 52), 32 tokens 5.3 us: bound by the instructions and latencies of
 // one round of waves, about 1000 instructions per four tokens.  Without the
 // settling of borders, its few 64-bit tokens made that 17 us.
 template <int Q, int KEY, bool BF16, bool FULL>
