@@ -610,15 +610,15 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
 #pragma unroll
         for (int q = 1; q < Q; ++q) d = max(d, key[q] - at);
         d = row_max(d);
-        if (i == r.k - 1) kth = at + d;
-        // none below: nothing (0) from here on
+        // none below: nothing (0) from here on, and no k-th, though the largest key wraps round to it
         at = d >= 0x80000000u ? at + d : 0;
+        if (i == r.k - 1) kth = at;
     }
     // bit Q - 1 - q: expert e0 + q is chosen
     uint32_t chosen = 0;
 #pragma unroll
     for (int q = 0; q < Q; ++q) chosen = __builtin_amdgcn_alignbit(chosen, (kth - 1u) - key[q], 31);
-    bool unsure = row_add(__popc(chosen)) != (uint32_t)r.k || kth <= 1u || kth >= 0x80000000u;
+    bool unsure = row_add(__popc(chosen)) != (uint32_t)r.k || kth <= 1u;
     if (KEY == KEY_SCORE) {
         const float x = from_key31(kth), y = at ? from_key31(at) : -INFINITY;
         unsure |= !(x - y > near + 4.76837158203125e-7f * fabsf(x));
