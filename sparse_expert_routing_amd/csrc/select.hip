@@ -692,12 +692,11 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
     if (mine && !doubt) {
         int32_t *io = idx + t * r.k + pos;
         float *wo = wts + t * r.k + pos;
-        const float c = sum == 0.f ? 0.f : r.scale / sum;
         for (uint32_t left = chosen << (32 - Q); left != 0;) {
             const int q = __clz(left);
             left &= ~(0x80000000u >> q);
             *io++ = e0 + q;
-            *wo++ = sc[wave][lane * Q + q] * c;
+            *wo++ = r.scale * (sc[wave][lane * Q + q] / sum);  // (scale / sum alone may be past fp32)
         }
     }
     wave_sync();
@@ -790,7 +789,7 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
         if (!on) e[i] = -1;
         le[i] = load_logit<BF16>(static_cast<const char *>(logits) + t * ld * (BF16 ? 2 : 4), on ? e[i] : 0);
         le[i] = on ? le[i] : -INFINITY;
-        d[i] = on ? r.scale * d[i] : 0.f;
+        d[i] = on ? d[i] : 0.f;
     }
     // the balance loss's coefficients of the row's sequence
     float f[Q], scale = 0.f;
@@ -851,11 +850,12 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
             cross += d[i] * share[i];
         }
         cross = row_sum(cross);
-        if (r.softmax && !r.renorm) mean = cross;
+        if (r.softmax && !r.renorm) mean = r.scale * cross;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= places) continue;
-            d[i] = share[i] * (r.renorm ? d[i] - cross : d[i]) * (r.softmax ? 1.f : sigmoid_f32(-le[i]));
+            // the scale behind the share: their product is the gradient's size, the scale's with dw may be past fp32
+            d[i] = r.scale * (share[i] * (r.renorm ? d[i] - cross : d[i]) * (r.softmax ? 1.f : sigmoid_f32(-le[i])));
             if (e[i] >= 0) row_acc[e[i]] = d[i];
         }
     }

@@ -51,3 +51,38 @@ def test_fewer_distinct_scores_than_choices(E, G, KG, gs):
     ri, _ = plain64.select(f64(l), f64(bias), k, "sigmoid", G, KG, gs)
     assert not np.isin(high.numpy(), ri[0]).all()  # the definition's choice is another one
     assert np.array_equal(idx.cpu().numpy(), ri)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,KG", [(1, 1), (32, 32), (32, 31)])
+def test_a_large_finite_scale_gives_finite_weights(score, G, KG):
+    """scale * (s / sum): the product of the scale and the sum's reciprocal alone may be past fp32."""
+    T, E, k, scale = 9, 64, 4, 1e30
+    say(f"[select-edges] scale {scale} {score} {KG} of {G}")
+    l = -27.0 - torch.rand(T, E, generator=torch.Generator().manual_seed(1))
+    for renorm in (True, False):
+        _, idx, w = select(l.cuda(), None, k, score=score, n_group=G, topk_group=KG, renorm=renorm, scale=scale)
+        ri, rw = plain64.select(f64(l), None, k, score, G, KG, "top2", renorm, scale)
+        assert np.array_equal(idx.cpu().numpy(), ri)
+        np.testing.assert_allclose(f64(w), rw, rtol=40 * plain64.EPS32)
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+def test_a_large_finite_scale_gives_finite_gradients(score, renorm):
+    """Two chosen experts with scores of about 1e-9 and weight gradients whose product with the scale is past fp32."""
+    T, E, k, scale = 5, 64, 8, 1e30
+    say(f"[select-edges] gradient with scale {scale} {score} {renorm}")
+    g = torch.Generator().manual_seed(3)
+    l = torch.randn(T, E, generator=g)
+    idx = torch.arange(k, dtype=torch.int32).repeat(T, 1)
+    l[:, :2] = -20.0
+    dw = torch.zeros(T, k)
+    dw[:, :2] = 1e10 * (1 + torch.rand(T, 2, generator=g))
+    sel = _lib.selection(T, E, k, score=score, renorm=renorm, scale=scale)
+    out = torch.full((T, E), float("nan"), device="cuda")
+    _lib.moe_select_backward(sel, l.cuda(), idx.cuda(), dw.cuda(), out)
+    ref = plain64.select_grad(f64(l), idx.numpy(), f64(dw), score, renorm, scale)
+    assert np.abs(ref).max() < 1e38
+    # products and sums of a row's E terms, exps of logits up to 24 below the largest
+    size = np.abs(ref).max(axis=1, keepdims=True)
+    assert (np.abs(f64(out) - ref) <= 80 * plain64.EPS32 * size).all()
