@@ -670,17 +670,22 @@ __global__ __launch_bounds__(256) void k_select_fast(SelectRule r, LaneMap map, 
     }
     const uint32_t count = __popc(chosen);
 
-    // the chosen scores' sum; one that underflows is left to the 64-bit code's way: a softmax's
-    // there is relative to the largest chosen, a sigmoid's keeps fp32's subnormals
+    // the chosen experts' scores as store_choice has them: fast_exp's error, enough to choose by, grows
+    // with the logit (2^-19 of the score at -32).  A sum that underflows is left to the 64-bit code's way: a
+    // softmax's there is relative to the largest chosen, a sigmoid's keeps fp32's subnormals
     float sum = 0.f;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        sum += (chosen >> (Q - 1 - q)) & 1 ? s[q] : 0.f;
-        sc[wave][lane * Q + q] = s[q];
+    for (int q = 0; q < Q; ++q) sc[wave][lane * Q + q] = l[q];
+    for (uint32_t left = chosen << (32 - Q); left != 0;) {
+        const int q = __clz(left);
+        left &= ~(0x80000000u >> q);
+        float &v = sc[wave][lane * Q + q];
+        v = r.softmax ? softmax_term(v, m) : sigmoid_f32(v);
+        sum += v;
     }
     sum = row_sum(sum);
     doubt |= r.renorm && !(sum > 1e-30f);
-    if (!r.renorm) sum = 1.f;
+    if (!r.renorm) sum = r.softmax ? total : 1.f;
     uint32_t pos = count;
     pos += row_shr<1>(pos);
     pos += row_shr<2>(pos);

@@ -86,3 +86,17 @@ def test_a_large_finite_scale_gives_finite_gradients(score, renorm):
     # products and sums of a row's E terms, exps of logits up to 24 below the largest
     size = np.abs(ref).max(axis=1, keepdims=True)
     assert (np.abs(f64(out) - ref) <= 80 * plain64.EPS32 * size).all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("G,KG", [(1, 1), (4, 4), (32, 32), (4, 3), (32, 31)])
+def test_weights_of_far_logits(G, KG, renorm):
+    """Sigmoids of logits down to -32.  Half steps: 2 for the exp, 1 each for the sum and quotient of a score; with
+    renormalisation the same for the denominator's, 1 for its sum of two, 1 for the quotient: 10 (4 without)."""
+    T, E, k = 4000, 64, 2
+    say(f"[select-edges] far logits, {KG} of {G} groups, renorm={renorm}")
+    l = -32.0 + 24.0 * torch.rand(T, E, generator=torch.Generator().manual_seed(7))
+    _, idx, w = select(l.cuda(), -l.mean(0).cuda(), k, n_group=G, topk_group=KG, renorm=renorm)
+    i = idx.cpu().numpy()
+    np.testing.assert_allclose(f64(w), plain64.weights(f64(l), i, "sigmoid", renorm, 1.0),
+                               rtol=(10 if renorm else 4) * plain64.EPS32, atol=0)
