@@ -268,7 +268,17 @@ __device__ __forceinline__ int row_rank(uint32_t v) {
 __device__ __forceinline__ uint32_t key31(float v) { return f32_order_key(v + 0.f) >> 1; }
 __device__ __forceinline__ float from_key31(uint32_t k) { return f32_from_order_key(k << 1); }
 
+// e^v to choose by: the product's rounding and log2(e)'s, each a half step of the exponent, are left in.
 __device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(1.4426950408889634f * v); }
+
+// e^v to two steps of fp32: what the exponent's rounding left out goes back to first order, e^c = 1 + c.  At most a
+// half step of an exponent that exp2 does not take to 0 or infinity, 2^-18; past those c can be anything, and only
+// its sign and finiteness are kept.
+__device__ __forceinline__ float exp_f32(float v) {
+    const float t = 1.44269502162933349609375f * v;  // log2(e) = this + 1.92596299e-8
+    const float c = __builtin_fmaf(v, 1.92596299e-8f, __builtin_fmaf(v, 1.44269502162933349609375f, -t));
+    return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(fminf(fmaxf(c, -1.f), 1.f), 0.693147182464599609375f, 1.f);
+}
 
 // The n <= Q experts from e0 on of a row that begins `at` elements into p, -inf
 // behind them (what is loaded there is another expert of the row).  vec: lanes
@@ -826,9 +836,9 @@ __global__ __launch_bounds__(256) void k_select_backward(SelectRule r, bool vec,
         for (int q = 0; q < Q; ++q) {
             // p becomes the score, x what gives a sigmoid's 1 - p = x p
             if (r.softmax) {
-                p[q] = m == -INFINITY ? 0.f : fast_exp(p[q] - m);
+                p[q] = m == -INFINITY ? 0.f : exp_f32(p[q] - m);
             } else {
-                x[q] = fast_exp(-p[q]);
+                x[q] = exp_f32(-p[q]);
                 p[q] = __builtin_amdgcn_rcpf(1.0f + x[q]);
             }
             total += p[q];
@@ -944,7 +954,7 @@ __global__ __launch_bounds__(512) void k_balance_part(SelectRule r, bool vec, in
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            p[q] = r.softmax ? (m == -INFINITY ? 0.f : fast_exp(p[q] - m)) : __builtin_amdgcn_rcpf(1.0f + fast_exp(-p[q]));
+            p[q] = r.softmax ? (m == -INFINITY ? 0.f : exp_f32(p[q] - m)) : __builtin_amdgcn_rcpf(1.0f + exp_f32(-p[q]));
             total += p[q];
         }
         total = row_sum(total);

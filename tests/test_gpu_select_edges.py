@@ -100,3 +100,34 @@ def test_weights_of_far_logits(G, KG, renorm):
     i = idx.cpu().numpy()
     np.testing.assert_allclose(f64(w), plain64.weights(f64(l), i, "sigmoid", renorm, 1.0),
                                rtol=(10 if renorm else 4) * plain64.EPS32, atol=0)
+
+
+def shares_tolerance(E, span):
+    """Half steps of a share p_e / sum p: an exp 4 (span: the rounding of l - m, relative to e^(l-m)), 1 + x 1, its
+    reciprocal 2, the same again for the denominator's terms, their sum over E / 16 of a lane and four exchanges, the
+    reciprocal of the sum 2 and the product 1."""
+    return (14 + 2 * span + E / 16 + 4 + 3) * plain64.EPS32
+
+
+def span_of(l, score):
+    return float((l.amax(1) - l.amin(1)).max()) if score == "softmax" else 0.0
+
+
+def far_logits(T, E, seed):
+    return -32.0 + 14.0 * torch.rand(T, E, generator=torch.Generator().manual_seed(seed))
+
+
+@pytest.mark.parametrize("E", [16, 13])
+def test_balance_loss_of_far_logits(E):
+    """One token and one choice per sequence: the loss is alpha E p_e, and shows the share's own error."""
+    T = 4000
+    say(f"[select-edges] balance loss, far logits E={E}")
+    l = far_logits(T, E, E)
+    idx = torch.randint(0, E, (T, 1), generator=torch.Generator().manual_seed(2)).to(torch.int32)
+    off = torch.arange(T + 1, dtype=torch.int32)
+    sel = _lib.selection(T, E, 1)
+    loss, load = torch.empty(T, device="cuda"), torch.empty(T, E, device="cuda")
+    ws = torch.empty(_lib.balance_workspace_bytes(sel, T), dtype=torch.uint8, device="cuda")
+    _lib.moe_balance_loss(sel, l.cuda(), idx.cuda(), off.cuda(), 0.5, loss, load, ws)
+    rl, _ = plain64.balance(f64(l), idx.numpy(), off.numpy(), 0.5, "sigmoid")
+    np.testing.assert_allclose(f64(loss), rl, rtol=shares_tolerance(E, 0) + plain64.EPS32, atol=0)
