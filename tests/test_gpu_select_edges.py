@@ -131,3 +131,117 @@ def test_balance_loss_of_far_logits(E):
     _lib.moe_balance_loss(sel, l.cuda(), idx.cuda(), off.cuda(), 0.5, loss, load, ws)
     rl, _ = plain64.balance(f64(l), idx.numpy(), off.numpy(), 0.5, "sigmoid")
     np.testing.assert_allclose(f64(loss), rl, rtol=shares_tolerance(E, 0) + plain64.EPS32, atol=0)
+
+
+def balance_grad_bound(l, off, load, dloss, alpha, score):
+    """What the balance gradient's elements may be off by: each is p'_e (f_e - sum_i f_i p'_i), times 1 - s_e for a
+    sigmoid, with p' the shares and f = alpha dloss (load - 1) / n: relative to the shares' errors and a few
+    roundings of each term, so to p'_e (|f_e| + sum |f| p')."""
+    T, E = l.shape
+    p = plain64.shares(f64(l), score)
+    rest = plain64.sigmoid(-f64(l)) if score == "sigmoid" else 1.0
+    size = np.zeros((T, E))
+    for q, (a, b) in enumerate(zip(off[:-1], off[1:])):
+        if b > a:
+            f = np.abs(alpha * dloss[q] * (load[q] - 1.0) / (b - a))
+            size[a:b] = f + (p[a:b] * f).sum(1, keepdims=True)
+    # two shares in a row (p' and the one inside the sum), the sum's E / 16 + 4 additions, f's 3 roundings and the
+    # difference, product and 1 - s (7) behind them
+    c = 2 * shares_tolerance(E, span_of(l, score)) + (E / 16 + 4 + 12) * plain64.EPS32
+    return c * p * rest * size + 1e-37
+
+
+BALANCE = [(300, 256, 8, "sigmoid", "f32", 5), (1000, 60, 4, "softmax", "bf16", 9), (1000, 64, 6, "softmax", "f32", 200),
+           (200, 1000, 20, "sigmoid", "bf16", 3), (5000, 256, 8, "sigmoid", "f32", 2), (4096, 8, 2, "softmax", "f32", 1),
+           (64, 17, 3, "sigmoid", "f32", 64), (501, 255, 8, "sigmoid", "f32", 4)]
+
+
+def sequences(T, n, seed):
+    cuts = torch.randint(0, T + 1, (n - 1,), generator=torch.Generator().manual_seed(seed)).sort().values
+    return torch.cat([torch.tensor([0]), cuts, torch.tensor([T])]).to(torch.int32)
+
+
+def balance_case(T, E, k, score, dtype, n):
+    g = torch.Generator().manual_seed(T + E)
+    l = (1.5 * torch.randn(T, E, generator=g)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    idx = torch.rand(T, E, generator=g).topk(k, dim=1).indices.sort(dim=1).values.to(torch.int32)
+    sel = _lib.selection(T, E, k, score=score, logits=dtype)
+    off = sequences(T, n, n)
+    loss, load = torch.empty(n, device="cuda"), torch.empty(n, E, device="cuda")
+    ws = torch.empty(_lib.balance_workspace_bytes(sel, n), dtype=torch.uint8, device="cuda")
+    _lib.moe_balance_loss(sel, l.cuda(), idx.cuda(), off.cuda(), 0.5, loss, load, ws)
+    return l, idx, sel, off, load, torch.rand(n, generator=g) + 0.5
+
+
+def check_balance_grad(l, got, off, load, dloss, alpha, score):
+    ref = plain64.select_grad(f64(l), None, None, score, True, 1.0, off.numpy(), f64(load), f64(dloss), alpha)
+    bound = balance_grad_bound(l, off.numpy(), f64(load), f64(dloss), alpha, score)
+    # a gradient of zeros would be found at nearly every element
+    inside = np.abs(ref) > 0
+    assert not inside.any() or (np.abs(ref) > bound)[inside].mean() > 0.95
+    assert (np.abs(got - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("T,E,k,score,dtype,n", BALANCE)
+def test_balance_gradient_in_its_own_size(T, E, k, score, dtype, n):
+    say(f"[select-edges] balance gradient T={T} E={E} {score} {dtype} n_seq={n}")
+    l, idx, sel, off, load, dloss = balance_case(T, E, k, score, dtype, n)
+    out = torch.full((T, E), float("nan"), device="cuda")
+    _lib.moe_select_backward(sel, l.cuda(), None, None, out, off.cuda(), load, dloss.cuda(), 0.5)
+    check_balance_grad(l, f64(out), off, load, dloss, 0.5, score)
+
+
+@pytest.mark.parametrize("E", [64, 61])
+def test_balance_gradient_of_far_logits(E):
+    say(f"[select-edges] balance gradient, far logits E={E}")
+    T, n = 700, 3
+    l, off = far_logits(T, E, E), sequences(T, n, 5)
+    sel = _lib.selection(T, E, 4)
+    load = 2 * torch.rand(n, E, generator=torch.Generator().manual_seed(1))
+    dloss = torch.ones(n)
+    out = torch.full((T, E), float("nan"), device="cuda")
+    _lib.moe_select_backward(sel, l.cuda(), None, None, out, off.cuda(), load.cuda(), dloss.cuda(), 0.5)
+    check_balance_grad(l, f64(out), off, load, dloss, 0.5, "sigmoid")
+
+
+@pytest.mark.parametrize("T,E,k,score,dtype,n", BALANCE)
+def test_balance_gradient_beside_the_weights(T, E, k, score, dtype, n):
+    """Both gradients in one call are the sum of each alone: the balance share, which may be far below the weights',
+    is found where no expert is chosen, and to one rounding of the sum where one is."""
+    say(f"[select-edges] both gradients T={T} E={E} {score} {dtype} n_seq={n}")
+    l, idx, sel, off, load, dloss = balance_case(T, E, k, score, dtype, n)
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(9)).cuda()
+    seq = dict(seq_offsets=off.cuda(), load=load, dloss=dloss.cuda(), alpha=0.5)
+    outs = [torch.full((T, E), float("nan"), device="cuda") for _ in range(3)]
+    for out, d, kw in zip(outs, (dw, None, dw), (seq, seq, {})):
+        _lib.moe_select_backward(sel, l.cuda(), idx.cuda() if d is not None else None, d, out, **kw)
+    both, loss, weights = (f64(o) for o in outs)
+    assert (loss != 0).mean() > 0.9
+    # renormalised weights: zero but for the chosen
+    assert (np.abs(both - (loss + weights)) <= 2 * plain64.EPS32 * (np.abs(loss) + np.abs(weights))).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_gradients_that_are_zero_by_definition(score):
+    """One renormalised choice has the weight `scale` whatever its logit; where every expert is chosen, every load is
+    1 and the loss alpha sum p' = alpha: no gradient, and none of the formula's roundings in its place."""
+    say(f"[select-edges] zero gradients {score}")
+    T, E = 133, 40
+    g = torch.Generator().manual_seed(4)
+    for seed in range(2):
+        l = torch.randn(T, E, generator=g).cuda()
+        sel, idx, w = select(l, None, 1, score=score, scale=2.5)
+        assert (w == 2.5).all()
+        out = torch.full((T, E), float("nan"), device="cuda")
+        _lib.moe_select_backward(sel, l, idx, torch.randn(T, 1, generator=g).cuda(), out)
+        assert (out == 0).all()
+        sel = _lib.selection(T, E, E, score=score)
+        idx = torch.arange(E, dtype=torch.int32).repeat(T, 1).cuda()
+        off = torch.tensor([0, 50, T], dtype=torch.int32, device="cuda")
+        loss, load = torch.empty(2, device="cuda"), torch.empty(2, E, device="cuda")
+        ws = torch.empty(_lib.balance_workspace_bytes(sel, 2), dtype=torch.uint8, device="cuda")
+        _lib.moe_balance_loss(sel, l, idx, off, 0.25, loss, load, ws)
+        assert (load == 1).all()
+        np.testing.assert_allclose(f64(loss), 0.25, rtol=shares_tolerance(E, 10) + plain64.EPS32)
+        _lib.moe_select_backward(sel, l, None, None, out.fill_(float("nan")), off, load, torch.ones(2, device="cuda"), 0.25)
+        assert (out == 0).all()
