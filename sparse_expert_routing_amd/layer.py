@@ -6,6 +6,8 @@ runs in the HIP kernels behind include/moe.h.
 """
 from __future__ import annotations
 
+from typing import NamedTuple, Optional
+
 import numpy as np
 import torch
 
@@ -22,6 +24,14 @@ def _dev(a, device):
     return t.to(device, non_blocking=False)
 
 
+class Checkpoint(NamedTuple):
+    """What MoeLayer.checkpoint() kept of a forward."""
+    x: tuple  # (values or codes, scales or None, format)
+    y_perm: tuple
+    routing: torch.Tensor  # as MoeLayer.routing
+    forward: Optional[int]  # whose buffers of the layer they are; None: they are the checkpoint's own
+
+
 class MoeLayer:
     """Weights and scratch of one layer; ``forward`` runs route -> dispatch ->
     expert FFN -> combine, ``update_bias`` the sign step, ``step`` both.
@@ -31,14 +41,16 @@ class MoeLayer:
     then computes the logits (kept in ``logits``) and chooses from them.
 
     A training step is ``forward``, ``checkpoint`` (what the backward needs of it, in 8
-    bits or as it is) and ``backward``; with a router also ``balance_loss``.  The routing
-    of the last forward is what they go by."""
+    bits or as it is) and ``backward``; with a router also ``balance_loss``.
+    ``checkpoint`` and ``balance_loss`` go by the last forward, ``backward`` by the
+    forward whose checkpoint it is given."""
 
     def __init__(self, T, d, I, act, wt, wr, experts: dict, shared: dict, E=256, k=8, device="cuda", router=None):
         self.T, self.d, self.I, self.E, self.k = T, d, I, E, k
         self.act, self.wt = act, wt
         self.device = torch.device(device)
         self.desc = _lib.desc(T, d, E, k, I, act, wt)
+        self.forwards = 0  # run so far: a checkpoint that reads the layer's own buffers knows whose they are
         self.sel = _lib.selection(T, E, k, **router) if router is not None else None
         self.wr = _dev(wr, self.device)
         self.ex = {n: (_dev(a, self.device) if a is not None else None) for n, a in experts.items()}
@@ -51,19 +63,23 @@ class MoeLayer:
         dev, T, d, E, k = self.device, self.T, self.d, self.E, self.k
         A = T * k
         i32 = dict(dtype=torch.int32, device=dev)
-        self.idx = torch.empty((T, k), **i32)
-        self.w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        # one buffer, so that a checkpoint's copy is one
+        self.routing = torch.empty(4 * A + (T * E if self.sel is not None else 0) + E + 1, **i32)
+        self.idx, self.w, self.offsets, self.row_src, self.row_of, self.logits = self._parts(self.routing)
         self.gap = torch.empty(T, dtype=torch.float32, device=dev)
         self.counts = torch.empty(E, **i32)
-        self.offsets = torch.empty(E + 1, **i32)
-        self.row_src = torch.empty(A, **i32)
-        self.row_of = torch.empty(A, **i32)
-        self.logits = torch.empty((T, E), dtype=torch.float32, device=dev) if self.sel is not None else None
         self.x_perm = self.x_perm_scale = None  # allocated on first use of the materialised dispatch
         self.y_perm = torch.empty((A, d), dtype=torch.float32 if self.wt == "f32" else torch.int16, device=dev)
         self.y = torch.empty((T, d), dtype=torch.float32, device=dev)
         ws = max(_lib.workspace_bytes(self.desc, s) for s in (0, 1, 2, 3, _lib.MOE_WS_ROUTER_LOGITS))
         self.ws = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+
+    def _parts(self, routing):
+        """idx, w, offsets, row_src, row_of and logits (None without a router) of a routing buffer."""
+        T, E, k = self.T, self.E, self.k
+        idx, w, row_src, row_of, logits, offsets = routing.split([T * k] * 4 + [routing.numel() - 4 * T * k - E - 1, E + 1])
+        return (idx.view(T, k), w.view(torch.float32).view(T, k), offsets, row_src, row_of,
+                logits.view(torch.float32).view(T, E) if self.sel is not None else None)
 
     def ensure_x_perm(self):
         if self.x_perm is None:
@@ -78,6 +94,7 @@ class MoeLayer:
         materialises x_perm and moe_expert_ffn consumes it.  Both give the
         same y bit for bit."""
         D = self.desc
+        self.forwards += 1
         if self.sel is None:
             _lib.moe_route(D, x, self.wr, bias, self.idx, self.w, self.gap if gap else None, self.ws, stream)
         else:
@@ -99,11 +116,12 @@ class MoeLayer:
         _lib.moe_combine(D, x, self.sh_w, self.y_perm, self.row_of, self.w, self.y, self.ws, stream)
         return self.y
 
-    def checkpoint(self, x, fmt="e4m3", stream=None):
-        """What the backward needs of the last forward: x and the routed outputs, in 8 bits ("e4m3" or "i8", half
-        the memory of "bf16", which keeps them as they are, the outputs until the next forward)."""
+    def checkpoint(self, x, fmt="e4m3", stream=None) -> Checkpoint:
+        """What the backward needs of the last forward: x and the routed outputs in 8 bits ("e4m3" or "i8", half the
+        memory of "bf16") and the routing, its own copies: any number of forwards may come before the backward.  "bf16"
+        keeps x and the layer's buffers themselves, which the next forward overwrites: backward() refuses it then."""
         if fmt == "bf16":
-            return (x, None, fmt), (self.y_perm, None, fmt)
+            return Checkpoint((x, None, fmt), (self.y_perm, None, fmt), self.routing, self.forwards)
         kept = []
         with torch.cuda.stream(stream):
             for t in (x, self.y_perm):
@@ -111,7 +129,7 @@ class MoeLayer:
                 scales = torch.empty((t.shape[0], (t.shape[1] + 127) // 128), dtype=torch.uint8, device=t.device)
                 _lib.moe_checkpoint_pack(t, codes, scales, fmt)
                 kept.append((codes, scales, fmt))
-        return tuple(kept)
+            return Checkpoint(*kept, self.routing.clone(), None)
 
     def balance_loss(self, seq_offsets, alpha, stream=None):
         """The last forward's sequence-wise balance loss [n_seq] and the loads [n_seq, E] that its gradient needs."""
@@ -126,9 +144,11 @@ class MoeLayer:
         return loss, load
 
     def backward(self, x, kept, dy, seq_offsets=None, load=None, dloss=None, alpha=0.0, stream=None) -> dict:
-        """Gradients of the last forward's output (dy [T, d] fp32), as moe_backward names them, from what checkpoint()
-        kept; x is read where there is a router, by its projection's gradient.  With a router, dloss [n_seq] adds the
-        gradient of balance_loss(seq_offsets, alpha)."""
+        """Gradients of a forward's output (dy [T, d] fp32), as moe_backward names them, from what checkpoint() kept of
+        that forward; x, its input, is read where there is a router, by its projection's gradient.  With a router, dloss
+        [n_seq] adds the gradient of balance_loss(seq_offsets, alpha) of that forward."""
+        if kept.forward not in (None, self.forwards):
+            raise ValueError("this checkpoint's routing and outputs were overwritten by a later forward: keep them in 8 bits")
         if self.sel is None and dloss is not None:
             raise ValueError("the balance loss needs a layer with a router")
         if dloss is None:
@@ -143,15 +163,16 @@ class MoeLayer:
         grads = {n: torch.empty(s, **f32) for n, s in (
             ("dx", (T, d)), ("dw_gate", (E, I, d)), ("dw_up", (E, I, d)), ("dw_down", (E, d, I)), ("ds_gate", (I, d)),
             ("ds_up", (I, d)), ("ds_down", (d, I)), ("dg", (T, k)), ("dw_router", (E, d)))}
-        xs, ys = (_lib.saved(*part) for part in kept)
+        xs, ys = _lib.saved(*kept.x), _lib.saved(*kept.y_perm)
+        idx, w, offsets, row_src, row_of, logits = self._parts(kept.routing)
         ws = torch.empty(_lib.workspace_bytes(D, _lib.MOE_WS_BACKWARD_SAVED), dtype=torch.uint8, device=self.device)
-        experts = (self.w, self.offsets, self.row_src, self.row_of, self.ex_w, self.sh_w, ys, dy)
+        experts = (w, offsets, row_src, row_of, self.ex_w, self.sh_w, ys, dy)
         if self.sel is None:
-            _lib.moe_backward_saved(D, xs, self.wr, self.idx, *experts, grads, ws)
+            _lib.moe_backward_saved(D, xs, self.wr, idx, *experts, grads, ws)
             return grads
         _lib.moe_backward_saved(D, xs, None, None, *experts, {n: g for n, g in grads.items() if n != "dw_router"}, ws)
         dlogits = torch.empty((T, E), **f32)
-        _lib.moe_select_backward(self.sel, self.logits, self.idx, grads["dg"], dlogits, seq_offsets, load, dloss, alpha)
+        _lib.moe_select_backward(self.sel, logits, idx, grads["dg"], dlogits, seq_offsets, load, dloss, alpha)
         ws = torch.empty(_lib.workspace_bytes(D, _lib.MOE_WS_ROUTER_GRAD), dtype=torch.uint8, device=self.device)
         _lib.moe_router_logits_backward(D, x, self.wr, dlogits, grads["dx"], grads["dx"], grads["dw_router"], ws)
         return grads
