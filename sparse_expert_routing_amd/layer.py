@@ -145,8 +145,9 @@ class MoeLayer:
 
     def backward(self, x, kept, dy, seq_offsets=None, load=None, dloss=None, alpha=0.0, stream=None) -> dict:
         """Gradients of a forward's output (dy [T, d] fp32), as moe_backward names them, from what checkpoint() kept of
-        that forward; x, its input, is read where there is a router, by its projection's gradient.  With a router, dloss
-        [n_seq] adds the gradient of balance_loss(seq_offsets, alpha) of that forward."""
+        that forward.  Where there is a router, its projection's gradient reads x, the forward's input, or with None the
+        checkpoint's values of it, so that x need not be kept beside them.  With a router, dloss [n_seq] adds the gradient
+        of balance_loss(seq_offsets, alpha) of that forward."""
         if kept.forward not in (None, self.forwards):
             raise ValueError("this checkpoint's routing and outputs were overwritten by a later forward: keep them in 8 bits")
         if self.sel is None and dloss is not None:
@@ -173,6 +174,11 @@ class MoeLayer:
         _lib.moe_backward_saved(D, xs, None, None, *experts, {n: g for n, g in grads.items() if n != "dw_router"}, ws)
         dlogits = torch.empty((T, E), **f32)
         _lib.moe_select_backward(self.sel, logits, idx, grads["dg"], dlogits, seq_offsets, load, dloss, alpha)
+        if x is None:
+            data, scales, fmt = kept.x
+            x = data if fmt == "bf16" else torch.empty((T, d), dtype=torch.bfloat16, device=self.device)
+            if fmt != "bf16":
+                _lib.moe_checkpoint_unpack(data, scales, fmt, x)
         ws = torch.empty(_lib.workspace_bytes(D, _lib.MOE_WS_ROUTER_GRAD), dtype=torch.uint8, device=self.device)
         _lib.moe_router_logits_backward(D, x, self.wr, dlogits, grads["dx"], grads["dx"], grads["dw_router"], ws)
         return grads

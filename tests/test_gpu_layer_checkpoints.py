@@ -106,3 +106,21 @@ def test_micro_batches_replay_from_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(ref, out):
             assert not equal(a, b), r
+
+
+@pytest.mark.parametrize("wt,fmt", [("bf16", "e4m3"), ("bf16", "i8"), ("e4m3", "i8"), ("bf16", "bf16")])
+def test_a_layer_with_a_router_can_do_without_its_input(wt, fmt):
+    """x None: the router projection's gradient takes the checkpoint's values too."""
+    say(f"[layer-checkpoints] no x {wt} {fmt}")
+    layer, xs, dys, bias = case("logits", wt)
+    x, dy = xs[0], dys[0]
+    layer.forward(x, bias)
+    kept = layer.checkpoint(x, fmt)
+    got = layer.backward(None, kept, dy)
+    if fmt == "bf16":
+        seen = x
+    else:
+        seen = torch.empty(x.shape, dtype=torch.bfloat16, device="cuda")
+        _lib.moe_checkpoint_unpack(kept[0][0], kept[0][1], fmt, seen)
+    assert not equal(layer.backward(seen, kept, dy), got)
+    assert not equal(layer.backward(x, kept, dy), {**got, "dw_router": layer.backward(x, kept, dy)["dw_router"]})
