@@ -373,6 +373,8 @@ def moe_select_backward(sel: Select, logits, idx, dweights, dlogits, seq_offsets
     """dlogits [T, E] through the weights (dweights [T, k], or None) and the balance loss (seq_offsets, load and dloss
     of moe_balance_loss, or None)."""
     c = _Call("moe_select_backward")
+    if seq_offsets is None and (load is not None or dloss is not None):
+        c.refuse("load and dloss need seq_offsets")
     p, ld = c.rows("logits", logits, sel.logits, (sel.T, sel.E))
     n = seq_offsets.numel() - 1 if seq_offsets is not None else 0
     on = seq_offsets is None
