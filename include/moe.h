@@ -367,7 +367,7 @@ typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP_TWO = 1 } moe_group_score_t;
  *   renorm       1: the weights are divided by their sum over the chosen
  *   scale        factor on the weights
  *   logits       moe_dtype_t of the logits: MOE_F32 or MOE_BF16
- * Any E up to 1024, k up to 64. */
+ * Any E up to 1024, k up to 64, T below 2^28 and T * k below 2^31. */
 typedef struct {
     int32_t T, E, k;
     int32_t score;
@@ -421,7 +421,7 @@ moe_status_t moe_select_backward(const moe_select_t *sel, const void *logits, in
  * A balanced sequence has the loss alpha.  load carries no gradient.
  *   idx         [T, k] the choices that are counted (moe_select's, or others)
  *   seq_offsets [n_seq + 1] int32 on the device, ascending, in [0, T]; empty
- *               sequences are allowed (loss 0, load 0)
+ *               sequences are allowed (loss 0, load 0); n_seq below 2^22
  *   loss [n_seq], load [n_seq, E] fp32 out
  *   workspace >= moe_balance_workspace_bytes(sel, n_seq) bytes, 16-byte aligned
  * Of the rule T, E, k, score and logits are read.  Deterministic.

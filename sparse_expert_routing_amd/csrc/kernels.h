@@ -210,7 +210,7 @@ struct SelectArgs {
     int32_t *idx;
     float *weights;
 };
-constexpr int kSelectMaxE = 1024, kSelectMaxK = 64;
+constexpr int kSelectMaxE = 1024, kSelectMaxK = 64, kSelectMaxT = 1 << 28;  // T: below it
 hipError_t launch_select(const SelectArgs &a, hipStream_t s);
 // The balance loss's share of the gradient (seq == nullptr: none).
 struct BalanceGrad {
@@ -232,6 +232,9 @@ struct SelectBackwardArgs {
 };
 hipError_t launch_select_backward(const SelectBackwardArgs &a, hipStream_t s);
 constexpr int kBalanceTokens = 64;  // tokens per workgroup of the loss's partial sums
+// Sequences: fewer, so that these workgroups (T / 64 and one per sequence, 512 threads) and
+// the sums' (one per sequence, 1024) are fewer than 2^32 threads.
+constexpr int kBalanceMaxSeq = 1 << 22;
 struct BalanceArgs {
     SelectRule rule;  // E, k and softmax are read
     int T;

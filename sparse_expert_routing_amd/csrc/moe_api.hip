@@ -110,7 +110,8 @@ moe_status_t check_select(const moe_select_t *s) {
     if (!(s->scale - s->scale == 0.f)) return MOE_EINVAL;  // infinite or NaN
     if (s->logits != MOE_F32 && s->logits != MOE_BF16) return s->logits == MOE_E4M3 ? MOE_ENOTSUP : MOE_EINVAL;
     if (s->E > moe::kSelectMaxE || s->k > moe::kSelectMaxK) return MOE_ENOTSUP;
-    if ((int64_t)s->T * s->k >= (1LL << 31)) return MOE_ENOTSUP;
+    // fewer than 2^32 threads to a launch, 16 of them per token
+    if ((int64_t)s->T * s->k >= (1LL << 31) || s->T >= moe::kSelectMaxT) return MOE_ENOTSUP;
     return MOE_OK;
 }
 
@@ -531,7 +532,7 @@ moe_status_t moe_select_backward(const moe_select_t *sel, const void *logits, in
 }
 
 size_t moe_balance_workspace_bytes(const moe_select_t *sel, int32_t n_seq) {
-    if (check_select(sel) != MOE_OK || n_seq <= 0) return 0;
+    if (check_select(sel) != MOE_OK || n_seq <= 0 || n_seq >= moe::kBalanceMaxSeq) return 0;
     return align_up(moe::balance_ws_bytes(sel->T, sel->E, n_seq));
 }
 
@@ -542,6 +543,7 @@ moe_status_t moe_balance_loss(const moe_select_t *sel, const void *logits, int64
     if (st != MOE_OK) return st;
     if (!logits || !idx || !seq_offsets || !loss || !load || n_seq <= 0 || ld < sel->E) return MOE_EINVAL;
     if (!aligned16(workspace)) return MOE_EINVAL;
+    if (n_seq >= moe::kBalanceMaxSeq) return MOE_ENOTSUP;
     if (!workspace || ws_bytes < moe_balance_workspace_bytes(sel, n_seq)) return MOE_EWORKSPACE;
     const moe::BalanceArgs a{rule_of(sel), sel->T, sel->logits == MOE_BF16, logits, ld, idx, seq_offsets, n_seq, alpha,
                              loss, load};
