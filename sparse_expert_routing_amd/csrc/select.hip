@@ -1083,16 +1083,23 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
 #undef FAST_KEY
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)(((int64_t)a.T + 3) / 4));
-#define GO(Q)                                                                                                        \
-    do {                                                                                                             \
-        if (a.bf16) hipLaunchKernelGGL((k_select<Q, true>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld, a.bias,   \
-                                       a.idx, a.weights);                                                            \
-        else hipLaunchKernelGGL((k_select<Q, false>), grid, block, 0, s, a.rule, a.T, a.logits, a.ld, a.bias, a.idx, \
-                                a.weights);                                                                          \
+    // (a wave per token: fewer than 2^32 threads to a launch)
+    constexpr int kRows = 1 << 25;
+    for (int t0 = 0; t0 < a.T; t0 += kRows) {
+        const int n = a.T - t0 < kRows ? a.T - t0 : kRows;
+        const dim3 grid((unsigned)((n + 3) / 4));
+        const void *logits = static_cast<const char *>(a.logits) + t0 * a.ld * (a.bf16 ? 2 : 4);
+        int32_t *idx = a.idx + (int64_t)t0 * r.k;
+        float *weights = a.weights + (int64_t)t0 * r.k;
+#define GO(Q)                                                                                                       \
+    do {                                                                                                            \
+        if (a.bf16) hipLaunchKernelGGL((k_select<Q, true>), grid, block, 0, s, r, n, logits, a.ld, a.bias, idx,     \
+                                       weights);                                                                    \
+        else hipLaunchKernelGGL((k_select<Q, false>), grid, block, 0, s, r, n, logits, a.ld, a.bias, idx, weights); \
     } while (0)
-    MOE_BY_WIDTH(GO, 64);
+        MOE_BY_WIDTH(GO, 64);
 #undef GO
+    }
     return hipGetLastError();
 }
 

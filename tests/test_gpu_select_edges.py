@@ -245,3 +245,18 @@ def test_gradients_that_are_zero_by_definition(score):
         np.testing.assert_allclose(f64(loss), 0.25, rtol=shares_tolerance(E, 10) + plain64.EPS32)
         _lib.moe_select_backward(sel, l, None, None, out.fill_(float("nan")), off, load, torch.ones(2, device="cuda"), 0.25)
         assert (out == 0).all()
+
+
+def test_more_tokens_than_one_launch_of_waves():
+    """A wave per token, 64 threads: 2^26 tokens and more in several launches, the last tokens as a call of their own."""
+    T, E, k, n = (1 << 26) + 7, 34, 2, 300
+    say(f"[select-edges] T={T} E={E}")
+    l = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_()
+    bias = torch.linspace(-0.05, 0.05, E).cuda()
+    kw = dict(n_group=17, topk_group=16)
+    _, idx, w = select(l, bias, k, **kw)
+    for part in (slice(0, n), slice((1 << 25) - n, (1 << 25) + n), slice(T - n, T)):
+        _, fi, fw = select(l[part].clone(), bias, k, **kw)
+        assert torch.equal(idx[part], fi) and torch.equal(w[part], fw)
+    ri, _ = plain64.select(f64(l[-n:]), f64(bias), k, "sigmoid", 17, 16)
+    assert np.array_equal(idx[-n:].cpu().numpy(), ri)
