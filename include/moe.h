@@ -477,7 +477,7 @@ moe_status_t moe_checkpoint_unpack(int64_t rows, int32_t cols, int32_t type, con
  *   dy_perm [T*k, d] bf16 out; rows that no entry names are left as they were
  *   dg      [T, k] fp32 out
  * dy, y_perm's data and dy_perm are 16-byte aligned.  d is a multiple of 64,
- * with bf16 weights too.  Deterministic.
+ * with bf16 weights too, T below 2^26, from d = 2048 on below 2^24.  Deterministic.
  */
 moe_status_t moe_combine_backward(const moe_desc_t *desc, const float *dy, const moe_saved_t *y_perm,
                                   const int32_t *row_of, const float *weights, void *dy_perm, float *dg, void *stream);

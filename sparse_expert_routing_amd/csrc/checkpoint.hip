@@ -389,6 +389,11 @@ hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s) {
 #undef MOE_CKPT_VARIANTS
 #undef MOE_CKPT_TYPES
 
+// Waves per token: four share a wide row.
+static int combine_waves(int d) { return d >= 2048 ? 4 : 1; }
+
+bool combine_backward_ok(int T, int d) { return (int64_t)T * combine_waves(d) < (1LL << 26); }
+
 hipError_t launch_combine_backward(int T, int d, const float *dy, const Saved &y, const int32_t *row_of,
                                    const float *weights, void *dyp, void *dys, float *dg, bool f32_out, hipStream_t s) {
     const int ntile = (d + kTile - 1) / kTile;
@@ -401,10 +406,10 @@ hipError_t launch_combine_backward(int T, int d, const float *dy, const Saved &y
         else hipLaunchKernelGGL((k_combine_backward<FMT, false, W>), grid, block, 0, s, T, d, ntile, dy, y,        \
                                 row_of, weights, dyp, dys, dg);                                                    \
     } while (0)
-#define GO(FMT)                     \
-    do {                            \
-        if (d >= 2048) GO_W(FMT, 4); \
-        else GO_W(FMT, 1);          \
+#define GO(FMT)                                  \
+    do {                                         \
+        if (combine_waves(d) == 4) GO_W(FMT, 4); \
+        else GO_W(FMT, 1);                       \
     } while (0)
     if (y.format == kCkptE4M3) GO(kCkptE4M3);
     else if (y.format == kCkptI8) GO(kCkptI8);

@@ -266,7 +266,9 @@ hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s);
 
 // dg[t, j] = dy[t] . y[row_of[t*8 + j]]; dyp row row_of[t*8 + j] = weights[t, j]
 // dy[t]; dys (nullptr: not written) row t = dy[t]; both bf16, or fp32 when
-// f32_out.  d a multiple of 64.
+// f32_out.  d a multiple of 64.  combine_backward_ok: whether one launch takes so many
+// tokens (fewer than 2^32 threads).
+bool combine_backward_ok(int T, int d);
 hipError_t launch_combine_backward(int T, int d, const float *dy, const Saved &y, const int32_t *row_of,
                                    const float *weights, void *dyp, void *dys, float *dg, bool f32_out, hipStream_t s);
 

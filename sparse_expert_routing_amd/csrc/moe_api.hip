@@ -462,6 +462,7 @@ moe_status_t moe_combine_backward(const moe_desc_t *d, const float *dy, const mo
     if (st != MOE_OK) return st;
     if (!dy || !row_of || !weights || !dy_perm || !dg || !saved_ok(y_perm)) return MOE_EINVAL;
     if (!aligned16(dy) || !aligned16(dy_perm)) return MOE_EINVAL;
+    if (!moe::combine_backward_ok(d->T, d->d)) return MOE_ENOTSUP;
     return hip_status(moe::launch_combine_backward(d->T, d->d, dy, to_internal(y_perm), row_of, weights, dy_perm, nullptr,
                                                    dg, false, static_cast<hipStream_t>(stream)));
 }

@@ -40,3 +40,10 @@ def test_the_largest_balance_workspace():
         assert L.moe_balance_loss(r, P, 4, P, P, n_seq, 0.1, P, P, P, need - 1, None) == _lib.MOE_EWORKSPACE
     assert L.moe_balance_workspace_bytes(r, n + 1) == 0
     assert L.moe_balance_loss(r, P, 4, P, P, n + 1, 0.1, P, P, P, 1 << 60, None) == _lib.MOE_ENOTSUP
+
+
+@pytest.mark.parametrize("T,d", [(1 << 26, 64), ((1 << 28) - 1, 1024), (1 << 24, 2048)])
+def test_more_tokens_than_the_combines_gradient_takes_are_refused(T, d):
+    """A wave of 64 threads per token, four from 2048 columns on, and fewer than 2^32 threads to a launch."""
+    L, ds, y = _lib.load(), _lib.desc(T, d, 256, 8, 128), _lib.Saved(P, P, 1)
+    assert L.moe_combine_backward(ctypes.byref(ds), P, ctypes.byref(y), P, P, P, P, None) == _lib.MOE_ENOTSUP
