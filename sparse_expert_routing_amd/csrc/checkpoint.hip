@@ -120,9 +120,15 @@ __device__ __forceinline__ TilePlace place_of(int64_t base, int ntile) {
 }
 
 // Tiles of a lane in flight: four of a large dense array, so that a wave has enough
-// loads under way (131072 x 7168 bf16 to e4m3 and back: 1053 us with one, 986 with
-// four); one otherwise, where there are too few tiles to fill the card so (2408
-// tiles: 4 us a pass with one, 8 with four) or places cost registers.
+// loads under way, one otherwise, where there are too few tiles to fill the card so
+// (2408 tiles: 4 us a pass with one, 8 with four) or places cost registers.  Four
+// against one, us, e4m3:
+//   bf16 there and back: 65536 tiles 12.3, 12.2 (the calls'), 131072 19.2, 19.8,
+//     524288 69.6, 71.3, 131072 x 7168 979, 993
+//   fp32 pack, whose loads are twice as long, always with one: 262144 tiles 25.5, 24.7,
+//     131072 x 7168 886, 809
+//   fp32 unpack, whose stores skip every other 16 bytes: 262144 tiles 53, 47, 1.8 million
+//     387, 364, 2.1 419, 420, 2.8 389, 551, 131072 x 7168 1091, 1477
 constexpr int kManyTiles = 65536;
 constexpr int unroll_of(bool flat) { return flat ? 4 : 1; }
 
@@ -356,26 +362,27 @@ unsigned tile_grid(int64_t tiles, bool flat) {
 
 }  // namespace
 
-#define MOE_CKPT_TYPES(KERNEL, FMT, ...)                                                                  \
+// F32_FLAT: whether KERNEL has a form for many fp32 tiles.
+#define MOE_CKPT_TYPES(KERNEL, F32_FLAT, FMT, ...)                                                        \
     do {                                                                                                  \
         if (a.bf16 && flat) hipLaunchKernelGGL((KERNEL<true, FMT, true, true>), __VA_ARGS__);             \
         else if (a.bf16 && vec) hipLaunchKernelGGL((KERNEL<true, FMT, true, false>), __VA_ARGS__);        \
         else if (a.bf16) hipLaunchKernelGGL((KERNEL<true, FMT, false, false>), __VA_ARGS__);              \
-        else if (flat) hipLaunchKernelGGL((KERNEL<false, FMT, true, true>), __VA_ARGS__);                 \
+        else if (flat) hipLaunchKernelGGL((KERNEL<false, FMT, true, F32_FLAT>), __VA_ARGS__);             \
         else if (vec) hipLaunchKernelGGL((KERNEL<false, FMT, true, false>), __VA_ARGS__);                 \
         else hipLaunchKernelGGL((KERNEL<false, FMT, false, false>), __VA_ARGS__);                         \
     } while (0)
-#define MOE_CKPT_VARIANTS(KERNEL, ...)                                                                    \
+#define MOE_CKPT_VARIANTS(KERNEL, F32_FLAT, ...)                                                          \
     do {                                                                                                  \
-        if (a.format == kCkptE4M3) MOE_CKPT_TYPES(KERNEL, kCkptE4M3, __VA_ARGS__);                        \
-        else MOE_CKPT_TYPES(KERNEL, kCkptI8, __VA_ARGS__);                                                \
+        if (a.format == kCkptE4M3) MOE_CKPT_TYPES(KERNEL, F32_FLAT, kCkptE4M3, __VA_ARGS__);              \
+        else MOE_CKPT_TYPES(KERNEL, F32_FLAT, kCkptI8, __VA_ARGS__);                                      \
     } while (0)
 
 hipError_t launch_checkpoint_pack(const CkptArgs &a, hipStream_t s) {
     const int ntile = (a.cols + kTile - 1) / kTile;
-    const bool vec = vec_ok(a, a.src), flat = vec && flat_ok(a);
+    const bool vec = vec_ok(a, a.src), flat = vec && a.bf16 && flat_ok(a);
     const dim3 grid(tile_grid(a.rows * ntile, flat)), block(256);
-    MOE_CKPT_VARIANTS(k_pack, grid, block, 0, s, a.rows, a.cols, ntile, a.src, a.ld, a.codes, a.scales);
+    MOE_CKPT_VARIANTS(k_pack, false, grid, block, 0, s, a.rows, a.cols, ntile, a.src, a.ld, a.codes, a.scales);
     return hipGetLastError();
 }
 
@@ -383,13 +390,16 @@ hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s) {
     const int ntile = (a.cols + kTile - 1) / kTile;
     const bool vec = vec_ok(a, a.dst), flat = vec && flat_ok(a);
     const dim3 grid(tile_grid(a.rows * ntile, flat)), block(256);
-    MOE_CKPT_VARIANTS(k_unpack, grid, block, 0, s, a.rows, a.cols, ntile, a.codes, a.scales, a.dst, a.ld);
+    MOE_CKPT_VARIANTS(k_unpack, true, grid, block, 0, s, a.rows, a.cols, ntile, a.codes, a.scales, a.dst, a.ld);
     return hipGetLastError();
 }
 #undef MOE_CKPT_VARIANTS
 #undef MOE_CKPT_TYPES
 
-// Waves per token: four share a wide row.
+// Waves per token: four share a wide row, whose one wave would have too few loads in
+// flight; they cost an exchange, and idle where 512 columns are all.  Four against one,
+// us, int8: T = 16384, d = 512 59, 47; 1024 95, 96; 1536 142, 146; 2048 190, 202; 4096
+// 379, 387; T = 2048, d = 1024 12.6, 12.1; 1536 16.9, 16.4; 2048 20.8, 20.9; 4096 46, 52.
 static int combine_waves(int d) { return d >= 2048 ? 4 : 1; }
 
 bool combine_backward_ok(int T, int d) { return (int64_t)T * combine_waves(d) < (1LL << 26); }
