@@ -3,10 +3,11 @@
 // A row is cut into tiles of 128 columns (the last may be shorter).  A tile has
 // one E8M0 scale 2^x, the smallest power of two at or above its largest
 // magnitude over the format's largest value (448 for e4m3, 127 for integers),
-// and a code per value: v / 2^x rounded to nearest even.  The quotient is exact,
-// so a code is off by half a step of its format and by nothing else: at most
-// 2^-4 of the value (e4m3, above its subnormals), 2^-7 of the tile's largest
-// (integers).  A tile that holds an infinity or a NaN gets scale byte 255, the
+// and a code per value: v / 2^x rounded to nearest even.  The quotient is exact, or
+// below fp32's normal numbers, where the code is 0 either way; so a code is off by
+// half a step of its format and by nothing else: at most 2^-4 of the value (e4m3,
+// above its subnormals), 1/127 of the tile's largest (integers: half of a scale that
+// is less than twice the largest over 127).  A tile that holds an infinity or a NaN gets scale byte 255, the
 // format's NaN, and reads back as NaN throughout: a lost activation shows.
 #include "device.h"
 #include "kernels.h"
