@@ -408,7 +408,9 @@ moe_status_t moe_select(const moe_select_t *sel, const void *logits, int64_t ld,
  *   seq_offsets  [n_seq + 1], load [n_seq, E]: from moe_balance_loss
  *   dloss        [n_seq] fp32: gradient of each sequence's loss
  *   alpha        as for moe_balance_loss
- * Rows outside every sequence get no balance gradient.
+ * Rows outside every sequence get no balance gradient.  Where a formula's gradient is
+ * zero whatever the logits, so is dlogits, exactly: one renormalised choice (its weight
+ * is the scale), and the loss where k = E (every load is 1, the loss alpha).
  */
 moe_status_t moe_select_backward(const moe_select_t *sel, const void *logits, int64_t ld, const int32_t *idx,
                                  const float *dweights, const int32_t *seq_offsets, int32_t n_seq, const float *load,

@@ -7,8 +7,9 @@
 // below fp32's normal numbers, where the code is 0 either way; so a code is off by
 // half a step of its format and by nothing else: at most 2^-4 of the value (e4m3,
 // above its subnormals), 1/127 of the tile's largest (integers: half of a scale that
-// is less than twice the largest over 127).  A tile that holds an infinity or a NaN gets scale byte 255, the
-// format's NaN, and reads back as NaN throughout: a lost activation shows.
+// is less than twice the largest over 127).  A tile that holds an infinity or a NaN
+// gets scale byte 255, the format's NaN, and reads back as NaN throughout: a lost
+// activation shows.
 #include "device.h"
 #include "kernels.h"
 

@@ -515,9 +515,10 @@ struct RgGrid {
     int dx_split, dx_tiles, dw_split, dw_tiles;
 };
 
-// Large problems, one launch each.  T = 16384, d = 7168: dx 235 us, 4.0 TB/s of what
-// it reads and writes; dw 148 us, the matrix cores 67% busy at 2.0 GHz; 420 us in
-// all with the terms and the sum (fp32 library products: 1247).  On one card each:
+// Large problems, one launch each.  T = 16384, d = 7168: dx 241 us at its fastest of ten
+// launches, 4.0 TB/s of what it reads and writes (267 on average, under the profiler),
+// dw 149 us (178), the matrix cores 67% busy at 2.0 GHz; 422 us in all with the terms
+// and the sum (fp32 library products: 1247).  On one card each:
 // both in one launch 548 against 522 us, dx with two workgroups of 64 columns on a CU
 // 551 against 506; dx's columns and tokens in even shares for all 256 CUs (224 have
 // work here) 475 against 479, not kept.

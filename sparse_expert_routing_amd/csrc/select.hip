@@ -483,8 +483,8 @@ __device__ __forceinline__ bool settle_border(uint32_t &near, int need, const fl
 // are nearer than 2^-20 (sigmoid) or 2^-17 (softmax) plus 2^-21 of their size: twice
 // those errors with room.  That is also where equal keys end up.
 //
-// 8 of 256 experts in 8 groups, biased sigmoid: 16384 tokens 12 us (17.8 MB; the wave
-// per token takes 52), 32 tokens 5.3 us: bound by the instructions and latencies of
+// 8 of 256 experts in 8 groups, biased sigmoid: 16384 tokens 13 us (17.8 MB; the wave
+// per token takes 52), 32 tokens 5.5 us: bound by the instructions and latencies of
 // one round of waves, about 1000 instructions per four tokens.  Without the
 // settling of borders, its few 64-bit tokens made that 17 us.
 template <int Q, int KEY, bool BF16, bool FULL>
@@ -766,7 +766,7 @@ __device__ __forceinline__ int sequence_of(const int32_t *__restrict__ off, int 
 // Sixteen lanes per token as in k_select_fast; the chosen experts' gradients, made
 // by the lanes of their places in idx, reach their experts through LDS.  dense:
 // every logit has a gradient; else the row is not read but for the chosen.
-// 16384 tokens of 256, weights and balance loss: 12.5 us for 34.6 MB; a wave per
+// 16384 tokens of 256, weights and balance loss: 13 us for 34.6 MB; a wave per
 // token took 17, and with each lane's experts side by side in memory (64 bytes
 // per lane, so that an instruction touched as many lines as lanes) 14.3.
 template <int Q, bool BF16>
