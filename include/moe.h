@@ -332,7 +332,7 @@ moe_status_t moe_backward(const moe_desc_t *desc, const void *x, const float *w_
  *   logits   [T, E]  fp32 out
  *   workspace >= moe_workspace_bytes(desc, MOE_WS_ROUTER_LOGITS) bytes of
  *            device memory (0 for fp32 activations; NULL allowed then)
- * x and logits are 16-byte aligned.
+ * x and logits are 16-byte aligned, d is below 2^23.
  */
 moe_status_t moe_router_logits(const moe_desc_t *desc, const void *x, const float *w_router, float *logits,
                                void *workspace, size_t ws_bytes, void *stream);
@@ -479,7 +479,8 @@ moe_status_t moe_checkpoint_unpack(int64_t rows, int32_t cols, int32_t type, con
  *   dy_perm [T*k, d] bf16 out; rows that no entry names are left as they were
  *   dg      [T, k] fp32 out
  * dy, y_perm's data and dy_perm are 16-byte aligned.  d is a multiple of 64,
- * with bf16 weights too, T below 2^26, from d = 2048 on below 2^24.  Deterministic.
+ * below 2^30, with bf16 weights too, T below 2^26, from d = 2048 on below 2^24.
+ * Deterministic.
  */
 moe_status_t moe_combine_backward(const moe_desc_t *desc, const float *dy, const moe_saved_t *y_perm,
                                   const int32_t *row_of, const float *weights, void *dy_perm, float *dg, void *stream);

@@ -263,6 +263,12 @@ class _Call:
     def refuse(self, what):
         raise MoeError(self.fn, MOE_EINVAL, "MOE_EINVAL: " + what)
 
+    def int32(self, name, n):
+        """A size that the C ABI takes in 32 bits."""
+        if n >= 1 << 31:
+            self.refuse(f"{name}, {n}, is not below 2^31")
+        return n
+
     def ptr(self, name, t, kind, shape, optional=False):
         """The address of a contiguous tensor of that type and shape."""
         if t is None:
@@ -376,7 +382,7 @@ def moe_select_backward(sel: Select, logits, idx, dweights, dlogits, seq_offsets
     if seq_offsets is None and (load is not None or dloss is not None):
         c.refuse("load and dloss need seq_offsets")
     p, ld = c.rows("logits", logits, sel.logits, (sel.T, sel.E))
-    n = seq_offsets.numel() - 1 if seq_offsets is not None else 0
+    n = c.int32("seq_offsets' count", seq_offsets.numel() - 1) if seq_offsets is not None else 0
     on = seq_offsets is None
     args = (c.ptr("idx", idx, "i32", (sel.T, sel.k), dweights is None),
             c.ptr("dweights", dweights, MOE_F32, (sel.T, sel.k), True),
@@ -392,7 +398,7 @@ def moe_balance_loss(sel: Select, logits, idx, seq_offsets, alpha, loss, load, w
     p, ld = c.rows("logits", logits, sel.logits, (sel.T, sel.E))
     if seq_offsets is None or seq_offsets.numel() < 2:
         c.refuse("seq_offsets holds no sequence")
-    n = seq_offsets.numel() - 1
+    n = c.int32("seq_offsets' count", seq_offsets.numel() - 1)
     args = (c.ptr("idx", idx, "i32", (sel.T, sel.k)), c.ptr("seq_offsets", seq_offsets, "i32", (n + 1,)), n, alpha,
             c.ptr("loss", loss, MOE_F32, (n,)), c.ptr("load", load, MOE_F32, (n, sel.E)))
     c.run(_library().moe_balance_loss, ctypes.byref(sel), p, ld, *args, *c.workspace(workspace), stream=stream)
@@ -402,6 +408,7 @@ def _plain_type(c, name, t):
     """MOE_F32 or MOE_BF16 of a plain 2-D tensor."""
     if t is None or t.dim() != 2:
         c.refuse(f"{name} has to be a matrix")
+    c.int32(f"{name}'s columns", t.shape[1])
     for kind in (MOE_F32, MOE_BF16):
         if t.dtype in _KINDS[kind]:
             return kind

@@ -462,7 +462,8 @@ moe_status_t moe_combine_backward(const moe_desc_t *d, const float *dy, const mo
     if (st != MOE_OK) return st;
     if (!dy || !row_of || !weights || !dy_perm || !dg || !saved_ok(y_perm)) return MOE_EINVAL;
     if (!aligned16(dy) || !aligned16(dy_perm)) return MOE_EINVAL;
-    if (!moe::combine_backward_ok(d->T, d->d)) return MOE_ENOTSUP;
+    // (the kernel's column index steps past d before it ends)
+    if (!moe::combine_backward_ok(d->T, d->d) || d->d >= (1 << 30)) return MOE_ENOTSUP;
     return hip_status(moe::launch_combine_backward(d->T, d->d, dy, to_internal(y_perm), row_of, weights, dy_perm, nullptr,
                                                    dg, false, static_cast<hipStream_t>(stream)));
 }
@@ -490,6 +491,7 @@ moe_status_t moe_router_logits(const moe_desc_t *d, const void *x, const float *
                                void *workspace, size_t ws_bytes, void *stream) {
     moe_status_t st = check_desc(d);
     if (st != MOE_OK) return st;
+    if (d->d >= (1 << 23)) return MOE_ENOTSUP;  // the weights' 32-bit index
     if (!x || !w_router || !logits || !aligned16(x) || !aligned16(logits)) return MOE_EINVAL;
     const size_t need = route_ws(d);
     if (need && (!workspace || ws_bytes < need)) return MOE_EWORKSPACE;
