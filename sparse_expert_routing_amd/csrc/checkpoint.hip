@@ -357,6 +357,9 @@ bool flat_ok(const CkptArgs &a) {
     return a.cols % kTile == 0 && a.ld == a.cols && a.rows * (a.cols / kTile) >= kManyTiles;
 }
 
+// Tiles of a row of any number of columns.
+int tiles_of(int cols) { return cols / kTile + (cols % kTile != 0); }
+
 unsigned tile_grid(int64_t tiles, bool flat) {
     const int64_t per = 16 * unroll_of(flat), n = (tiles + per - 1) / per;
     return (unsigned)(n < (1 << 22) ? n : (1 << 22));
@@ -381,7 +384,7 @@ unsigned tile_grid(int64_t tiles, bool flat) {
     } while (0)
 
 hipError_t launch_checkpoint_pack(const CkptArgs &a, hipStream_t s) {
-    const int ntile = (a.cols + kTile - 1) / kTile;
+    const int ntile = tiles_of(a.cols);
     const bool vec = vec_ok(a, a.src), flat = vec && a.bf16 && flat_ok(a);
     const dim3 grid(tile_grid(a.rows * ntile, flat)), block(256);
     MOE_CKPT_VARIANTS(k_pack, false, grid, block, 0, s, a.rows, a.cols, ntile, a.src, a.ld, a.codes, a.scales);
@@ -389,7 +392,7 @@ hipError_t launch_checkpoint_pack(const CkptArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_checkpoint_unpack(const CkptArgs &a, hipStream_t s) {
-    const int ntile = (a.cols + kTile - 1) / kTile;
+    const int ntile = tiles_of(a.cols);
     const bool vec = vec_ok(a, a.dst), flat = vec && flat_ok(a);
     const dim3 grid(tile_grid(a.rows * ntile, flat)), block(256);
     MOE_CKPT_VARIANTS(k_unpack, true, grid, block, 0, s, a.rows, a.cols, ntile, a.codes, a.scales, a.dst, a.ld);
@@ -408,7 +411,7 @@ bool combine_backward_ok(int T, int d) { return (int64_t)T * combine_waves(d) < 
 
 hipError_t launch_combine_backward(int T, int d, const float *dy, const Saved &y, const int32_t *row_of,
                                    const float *weights, void *dyp, void *dys, float *dg, bool f32_out, hipStream_t s) {
-    const int ntile = (d + kTile - 1) / kTile;
+    const int ntile = tiles_of(d);
     const dim3 block(256);
 #define GO_W(FMT, W)                                                                                               \
     do {                                                                                                           \
