@@ -378,8 +378,8 @@ typedef struct {
 } moe_select_t;
 
 /*
- * The choice and its combine weights, in one launch (from 2^25 tokens on, several
- * where E is above 512 or more than 16 groups compete).
+ * The choice and its combine weights, in one launch (past 2^25 tokens in several,
+ * for rules that a wave per token takes).
  *   logits  [T, E], row t at logits + t * ld (ld >= E, in elements)
  *   bias    [E] fp32 or NULL: added to the scores for the choice only
  *   idx     [T, k] int32 out: ids ascending; the k largest s + bias among the
