@@ -43,7 +43,7 @@ constexpr int kPanel = 128;      // columns of a word of scales
 constexpr int kTable = 264 * 4;  // row tiles before every fourth group
 constexpr int kQueue = 4;        // tiles between the loads and the products, at most NS + 1
 constexpr int kGroupM = 8;       // row tiles side by side
-// An offset past the end of every resource.
+// An offset past the end of every resource (nothing may be added to it).
 constexpr uint32_t kOob = 0xFFFF0000u;
 
 enum { MX_BF16 = 0, MX_F32 = 1, MX_SWIGLU = 2 };
@@ -669,10 +669,11 @@ __global__ __launch_bounds__((64 * Cfg<AF, BM>::W), (Cfg<AF, BM>::WGS)) void k_m
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const uint32_t row = (uint32_t)arow(i);
-                const uint32_t at0 = row < (uint32_t)rows ? row * orow : kOob;
+                // (rows past the tile's begin at the resource's end: with a column's offset
+                // on top, at most 2^31 + 2^23, they stay behind it, where kOob would wrap)
+                const uint32_t at0 = min(row, (uint32_t)rows) * orow;
                 auto at16 = [&](int h) {  // of the row that a lane holds a part of behind swap16
-                    const uint32_t r = row - (uint32_t)(16 * odd) + (uint32_t)(16 * h);
-                    return r < (uint32_t)rows ? r * orow : kOob;
+                    return min(row - (uint32_t)(16 * odd) + (uint32_t)(16 * h), (uint32_t)rows) * orow;
                 };
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
