@@ -199,13 +199,16 @@ class MoeLayer:
     def pack_experts(self, fmt="e4m3", keep=True, stream=None):
         """The routed experts' weights (bf16) as they are now in four bits (MX e2m1), for the forwards from here on; x and
         the experts' inner activations are packed in fmt, "e4m3" or "e2m1".  Called again it packs anew, in place (what a
-        graph captured stays what it was captured with); adamw_step does.  keep=False lets go of the bf16 weights: the layer
-        then only serves."""
+        graph captured stays what it was captured with); adamw_step does.  keep=False lets go of the bf16 weights, once all that
+        was launched and may read them has ended (not while a graph is captured): the layer then only serves, and a graph
+        that captured them is not replayed any more."""
         if self.wt != "bf16":
             raise ValueError(f"experts are packed from bf16 weights, not {self.wt}")
         self._need_weights()
         if fmt not in _lib.MX_FORMATS:
             raise ValueError(f"format {fmt!r}")
+        if not keep and torch.cuda.is_current_stream_capturing():
+            raise ValueError("the experts' bf16 weights cannot be let go of while a graph is captured")
         E, T, d, I, A = self.E, self.T, self.d, self.I, self.T * self.k
         with torch.cuda.stream(stream):
             if fmt not in self._packed_room:
@@ -221,6 +224,9 @@ class MoeLayer:
                 _lib.moe_mx_pack(self.ex[n].view(-1, 2 * codes.shape[2]), codes.view(-1, codes.shape[2]), scales, "e2m1")
         self.packed = (fmt, mats)
         if not keep:
+            # the packing on its stream, and forwards on any other: freed before those have read them, the weights' memory
+            # would be handed out anew on the stream that they were allocated on
+            torch.cuda.synchronize(self.device)
             self.ex.update(gate=None, up=None, down=None)
             self.ex_w = None
 
