@@ -527,7 +527,7 @@ typedef struct {
 } moe_mx_t;
 
 /*
- * Values to microscaled codes and back, rows and columns of any number.
+ * Values to microscaled codes and back, one row and column or more.
  *   type     MOE_F32 or MOE_BF16: of src and dst
  *   src, dst [rows, cols], row r at + r * ld (ld >= cols, in elements); what
  *            lies between the rows is neither read nor written
@@ -547,8 +547,8 @@ moe_status_t moe_mx_unpack(int64_t rows, int32_t cols, int32_t type, const uint8
                            int32_t format, void *dst, int64_t ld, void *stream);
 
 /* Rows in G groups of any sizes, each with a matrix of its own.
- *   M      rows of the output
- *   x_rows rows of x
+ *   M      rows of the output, from 1 on (a call of none is left out)
+ *   x_rows rows of x, from 1 on
  *   k      row r of the product reads row row_src[r] / k of x (with row_src;
  *          without, k = 1, x_rows = M and row r reads row r) */
 typedef struct {

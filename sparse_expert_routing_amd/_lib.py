@@ -368,6 +368,19 @@ class _Call:
             self.on("the workspace", t)
         return t.data_ptr(), t.numel() * t.element_size()
 
+    def nothing(self, stream):
+        """A call of no rows: where run would look, and no launch."""
+        if self.elsewhere is not None:
+            self.refuse(self.elsewhere)
+        if stream is not None and stream.device.index != self.index:
+            self.refuse(f"the stream is on {stream.device}, not cuda:{self.index}")
+
+    def no_rows(self, x_rows, row_src, k, stream):
+        """A product of no rows (a shard that no token chose), which the C ABI does not take: nothing, if its x is fit for it."""
+        if k < 1 or (row_src is None and (k != 1 or x_rows != 0)):
+            self.refuse(f"x's {x_rows} rows and k = {k} are not those of no rows")
+        self.nothing(stream)
+
     def run(self, call, *args, stream=None):
         if self.elsewhere is not None:
             self.refuse(self.elsewhere)
@@ -541,12 +554,14 @@ def _mx_matrix(c, codes, scales, fmt, rows, cols):
 
 def moe_mx_pack(src, codes, scales, fmt, stream=None):
     """src [rows, cols] (fp32 or bf16, any row stride) as microscaled codes [rows, cols] ("e4m3") or [rows, ceil(cols/2)]
-    ("e2m1") and scales [ceil(cols/128), rows, 4]."""
+    ("e2m1") and scales [ceil(cols/128), rows, 4].  No rows are allowed."""
     c = _Call("moe_mx_pack")
     kind = _plain_type(c, "src", src)
     rows, cols = src.shape
     p, ld = c.rows("src", src, kind, (rows, cols))
     q, s = _mx_matrix(c, codes, scales, fmt, rows, cols)
+    if rows == 0:  # (the C ABI takes no empty matrix)
+        return c.nothing(stream)
     c.run(load().moe_mx_pack, rows, cols, kind, p, ld, MX_FORMATS[fmt], q, s, stream=stream)
 
 
@@ -557,6 +572,8 @@ def moe_mx_unpack(codes, scales, fmt, dst, stream=None):
     rows, cols = dst.shape
     q, s = _mx_matrix(c, codes, scales, fmt, rows, cols)
     p, ld = c.rows("dst", dst, kind, (rows, cols))
+    if rows == 0:  # (the C ABI takes no empty matrix)
+        return c.nothing(stream)
     c.run(load().moe_mx_unpack, rows, cols, kind, q, s, MX_FORMATS[fmt], p, ld, stream=stream)
 
 
@@ -603,20 +620,22 @@ def _mx_rows(c, x, K, M, row_src, k):
 
 def moe_mx_product(x: Mx, w: Mx, offsets, out, workspace=None, row_src=None, k=1, stream=None):
     """out [M, N] (fp32 or bf16): rows offsets[g] .. offsets[g+1] are x's (row r: x's row r, or row_src[r] // k) times
-    w[g]^T, w [G, N, K] in four bits."""
+    w[g]^T, w [G, N, K] in four bits.  M = 0 is allowed (a shard that no token chose)."""
     c = _Call("moe_mx_product")
     G, N, K = _mx_weights(c, "w", w)
     kind = _plain_type(c, "out", out)
     M = c.int32("out's rows", out.shape[0])
     rows, src = _mx_rows(c, x, K, M, row_src, k)
     args = (c.ptr("offsets", offsets, "i32", (G + 1,)), ctypes.byref(w), kind, c.ptr("out", out, kind, (M, N)))
+    if M == 0:
+        return c.no_rows(rows, row_src, k, stream)
     c.run(load().moe_mx_product, ctypes.byref(MxGroups(G, M, N, K, rows, k)), ctypes.byref(x), src, *args,
           *c.workspace(workspace), stream=stream)
 
 
 def moe_mx_expert_ffn(x: Mx, gate: Mx, up: Mx, down: Mx, offsets, y, workspace, row_src=None, k=1, stream=None):
     """The routed experts' SwiGLU FFN on weights in four bits (gate, up [G, I, d], down [G, d, I]): y [M, d] bf16 for
-    the rows of moe_mx_product; h is packed in x's format."""
+    the rows of moe_mx_product (or none); h is packed in x's format."""
     c = _Call("moe_mx_expert_ffn")
     G, I, d = _mx_weights(c, "gate", gate)
     _mx_weights(c, "up", up, (G, I, d))
@@ -627,6 +646,8 @@ def moe_mx_expert_ffn(x: Mx, gate: Mx, up: Mx, down: Mx, offsets, y, workspace, 
     rows, src = _mx_rows(c, x, d, M, row_src, k)
     args = (c.ptr("offsets", offsets, "i32", (G + 1,)), ctypes.byref(gate), ctypes.byref(up), ctypes.byref(down),
             c.ptr("y", y, MOE_BF16, (M, d)))
+    if M == 0:
+        return c.no_rows(rows, row_src, k, stream)
     c.run(load().moe_mx_expert_ffn, ctypes.byref(MxGroups(G, M, I, d, rows, k)), ctypes.byref(x), src, *args,
           *c.workspace(workspace), stream=stream)
 
