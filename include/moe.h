@@ -657,7 +657,9 @@ typedef struct {
 /*
  * The step of `count` tensors (read on the host before the call returns), in one
  * launch for every 59 of the same types or more.  Tensors of no elements are allowed;
- * pointers are aligned as their type; n below 2^35.  Deterministic.
+ * pointers are aligned as their type; n below 2^35.  What a call writes overlaps with
+ * nothing else of it (the workgroups would race; the binding refuses it): a weight that
+ * is used twice is one tensor.  Deterministic.
  */
 moe_status_t moe_adamw(const moe_adamw_t *rule, const moe_adamw_tensor_t *tensors, int32_t count, void *stream);
 

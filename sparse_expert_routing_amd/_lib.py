@@ -664,7 +664,8 @@ class AdamWTensors:
 def adamw_tensors(weights, grads, m, v, m_scales=None, v_scales=None, masters=None) -> AdamWTensors:
     """Lists of contiguous tensors of equal length each: weights and gradients in fp32 or bf16; states in fp32, or in
     8 bits (uint8 codes) with m_scales and v_scales [ceil(n/128)]; masters: fp32 weights that the step works on (an entry
-    or the list may be None).  Made once for the tensors of a model, for moe_adamw."""
+    or the list may be None).  What a step writes may not overlap with anything else of it: a weight that a model uses
+    twice is listed once.  Made once for the tensors of a model, for moe_adamw."""
     c = _Call("moe_adamw")
     n = len(weights)
     empty = [None] * n
@@ -689,9 +690,26 @@ def adamw_tensors(weights, grads, m, v, m_scales=None, v_scales=None, masters=No
             c.ptr(f"m {i}", mi, state, w.shape), c.ptr(f"v {i}", vi, state, w.shape),
             c.ptr(f"m's scales {i}", ms, MOE_E4M3, tiles, wide), c.ptr(f"v's scales {i}", vs, MOE_E4M3, tiles, wide),
             c.ptr(f"master {i}", ma, MOE_F32, w.shape, True), w.numel(), kinds[0], kinds[1], 32 if wide else 8)
+    _apart(c, lists)
     if c.elsewhere is not None:
         c.refuse(c.elsewhere)
     return AdamWTensors(table, c.index, lists)
+
+
+def _apart(c, lists):
+    """Refuses a step that writes what it reads or writes elsewhere (its workgroups would race)."""
+    names = ("weight", "gradient", "m", "v", "m's scales", "v's scales", "master")
+    places = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), k, i)
+                    for k, ts in enumerate(lists) for i, t in enumerate(ts) if t is not None and t.numel())
+    last = written = (0, 0, 0, 0)  # those that reach furthest, of all so far and of those that the step writes
+    for p in places:
+        other = written if p[2] == 1 else last
+        if p[0] < other[1]:
+            c.refuse(f"{names[p[2]]} {p[3]} and {names[other[2]]} {other[3]} overlap")
+        if p[1] > last[1]:
+            last = p
+        if p[2] != 1 and p[1] > written[1]:
+            written = p
 
 
 def moe_adamw(tensors: AdamWTensors, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, step=1, seed=0, grad_scale=None,
