@@ -377,7 +377,7 @@ class _Call:
 
     def no_rows(self, x_rows, row_src, k, stream):
         """A product of no rows (a shard that no token chose), which the C ABI does not take: nothing, if its x is fit for it."""
-        if k < 1 or (row_src is None and (k != 1 or x_rows != 0)):
+        if row_src is None and (k != 1 or x_rows != 0):
             self.refuse(f"x's {x_rows} rows and k = {k} are not those of no rows")
         self.nothing(stream)
 
@@ -578,10 +578,14 @@ def moe_mx_unpack(codes, scales, fmt, dst, stream=None):
 
 
 def mx_product_workspace_bytes(G, M, N, K, out="bf16") -> int:
+    if max(G, M, N, K) >= 1 << 31:  # (past the C ABI's 32 bits: no product that it takes)
+        return 0
     return load().moe_mx_product_workspace_bytes(ctypes.byref(MxGroups(G, M, N, K, M, 1)), DTYPES[out])
 
 
 def mx_ffn_workspace_bytes(E, M, d, I, fmt) -> int:
+    if max(E, M, d, I) >= 1 << 31:
+        return 0
     return load().moe_mx_ffn_workspace_bytes(ctypes.byref(MxGroups(E, M, I, d, M, 1)), MX_FORMATS[fmt])
 
 
@@ -615,6 +619,8 @@ def _mx_rows(c, x, K, M, row_src, k):
         c.ptr("x's codes", codes, "byte", wide)
     if not c.fits(scales, MOE_E4M3, scale):
         c.ptr("x's scales", scales, MOE_E4M3, scale)
+    if not 0 < k < 1 << 31:
+        c.refuse(f"k, {k}, is not from 1 to 2^31 - 1")
     return c.int32("x's rows", rows), None if row_src is None else c.ptr("row_src", row_src, "i32", (M,))
 
 
@@ -724,6 +730,8 @@ def moe_adamw(tensors: AdamWTensors, lr, betas=(0.9, 0.999), eps=1e-8, weight_de
     if n == 0:
         return
     on_device = [hasattr(t, "data_ptr") for t in (lr, step)]
+    if not on_device[1] and not 0 < step < 1 << 63:
+        c.refuse(f"step, {step}, is not from 1 to 2^63 - 1")
     rule = AdamW(0.0 if on_device[0] else lr, betas[0], betas[1], eps, weight_decay, 1 if on_device[1] else step,
                  seed & 0xFFFFFFFFFFFFFFFF,
                  c.ptr("grad_scale", grad_scale, MOE_F32, (1,)) if grad_scale is not None else None,
