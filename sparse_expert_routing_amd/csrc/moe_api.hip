@@ -228,6 +228,8 @@ moe_status_t check_adamw(const moe_adamw_t *r) {
     if (r->eps != 0.0 && !(r->eps >= 0x1p-126 && r->eps <= 0x1p126)) return MOE_EINVAL;
     if (!(r->beta1 >= 0.0 && r->beta1 < 1.0) || !(r->beta2 >= 0.0 && r->beta2 < 1.0)) return MOE_EINVAL;
     if (r->step_ptr == nullptr && r->step < 1) return MOE_EINVAL;
+    // (read through the scalar cache, which drops an address's low bits)
+    if (!aligned4(r->grad_scale) || !aligned4(r->lr_ptr) || reinterpret_cast<uintptr_t>(r->step_ptr) % 8) return MOE_EINVAL;
     return MOE_OK;
 }
 moe_status_t check_adamw_tensor(const moe_adamw_tensor_t *t) {
