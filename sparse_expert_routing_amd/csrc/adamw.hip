@@ -22,8 +22,7 @@
 // weights without a master, fp32 gradients: 3.2 ms, 5.4 TB/s (4.9 ms with two exact roots,
 // an exact division and rounding in integers); 0.81 x 10^9 with masters and fp32 states:
 // 4.3 to 4.5 ms, 5.4 to 5.7 TB/s.
-#include "device.h"
-#include "kernels.h"
+#include "mx.h"
 
 #include <math.h>
 #include <type_traits>
@@ -138,11 +137,8 @@ __device__ __forceinline__ float root(float v) {
     return tiny ? r * 0x1p-32f : r;
 }
 
-__device__ __forceinline__ float pow2_of_byte(uint32_t b) {
-    return b == 255u ? __uint_as_float(0x7fc00000u) : b == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
-}
 __device__ __forceinline__ void decode8(uint2 w, uint32_t byte, float (&v)[8]) {
-    const float s = pow2_of_byte(byte);
+    const float s = e8m0_value(byte);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int x = (int)(h ? w.y : w.x);

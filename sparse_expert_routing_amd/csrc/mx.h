@@ -24,10 +24,8 @@ __device__ __forceinline__ uint32_t mx_block_byte(uint32_t amax_bits) {
 __device__ __forceinline__ float e8m0_value(uint32_t b) {
     return b == 255u ? __uint_as_float(0x7fc00000u) : b == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
 }
-// 2^-x of a scale byte 1 .. 254.
-__device__ __forceinline__ float e8m0_inverse(uint32_t b) {
-    return b == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - b) << 23);
-}
+// 2^-x of a scale byte 1 .. 253 (a finite block's is 253 at most).
+__device__ __forceinline__ float e8m0_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 
 // Values of at most 6 as e2m1 codes, rounded to nearest even: codes of a and b in byte
 // SEL of w (which keeps its other bytes), a's in the low half.

@@ -75,6 +75,7 @@ struct Cfg {
     static constexpr int WM = BM >= 64 ? W / 2 : 1, WN = W / WM;                // waves over rows and weight rows
     static constexpr int TM = BM / 32 / WM, TN = BN / 32 / WN;                  // 32 x 32 blocks of a wave
     static_assert((NS == 3 && S == 2) || (NS == 2 && S == 4), "which steps load");
+    static_assert(TM == 4 || TM == 1, "the products' loops by the row blocks with rows in them");
     static_assert(NS >= 2 && NS + 1 <= kQueue && (NS - 1) * L < 64, "the ring, and the counter of loads");
 };
 
@@ -591,10 +592,6 @@ __global__ __launch_bounds__((64 * Cfg<AF, BM>::W), (Cfg<AF, BM>::WGS)) void k_m
             if (nb >= 4) run(Int<4>{});
             else if (nb == 3) run(Int<3>{});
             else if (nb == 2) run(Int<2>{});
-            else if (nb == 1) run(Int<1>{});
-            else run(Int<0>{});
-        } else if constexpr (TM == 2) {
-            if (nb >= 2) run(Int<2>{});
             else if (nb == 1) run(Int<1>{});
             else run(Int<0>{});
         } else {
