@@ -25,6 +25,7 @@ SCORES = {"sigmoid": MOE_SIGMOID, "softmax": MOE_SOFTMAX}
 GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP_TWO}
 MOE_MX_E4M3, MOE_MX_E2M1 = 0, 1
 MX_FORMATS = {"e4m3": MOE_MX_E4M3, "e2m1": MOE_MX_E2M1}
+MX_GATHERED_BYTES = (1 << 32) - (1 << 20)  # of x's codes, at most, where its rows are gathered
 SAVED_FORMATS = {"bf16": MOE_SAVED_BF16, "e4m3": MOE_SAVED_E4M3, "i8": MOE_SAVED_I8}
 
 EXPORTS = ("moe_route", "moe_dispatch", "moe_dispatch_noalloc", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_gate_up_rows",

@@ -210,9 +210,12 @@ class MoeLayer:
         if not keep and torch.cuda.is_current_stream_capturing():
             raise ValueError("the experts' bf16 weights cannot be let go of while a graph is captured")
         E, T, d, I, A = self.E, self.T, self.d, self.I, self.T * self.k
+        need = _lib.mx_ffn_workspace_bytes(E, A, d, I, fmt)
+        if need == 0 or T * _lib.mx_code_bytes(d, fmt) > _lib.MX_GATHERED_BYTES:  # (found out before any weights are let go of)
+            raise ValueError(f"{T} tokens of {d} in {fmt} are more than moe_mx_expert_ffn takes")
         with torch.cuda.stream(stream):
             if fmt not in self._packed_room:
-                ws = torch.empty(_lib.mx_ffn_workspace_bytes(E, A, d, I, fmt), dtype=torch.uint8, device=self.device)
+                ws = torch.empty(need, dtype=torch.uint8, device=self.device)
                 self._packed_room[fmt] = (*_lib.mx_empty(T, d, fmt, self.device), ws)
             mats = self.packed[1] if self.packed is not None else []
             if not mats:

@@ -31,3 +31,12 @@ def test_weights_are_not_let_go_of_in_a_capture(layer, monkeypatch):
         layer.pack_experts(keep=False)
     assert layer.ex_w is not None and layer.packed is None
     layer.pack_experts()
+
+
+@pytest.mark.parametrize("T,fmt", [(1 << 25, "e4m3"), ((1 << 26) - 100, "e2m1"), (1 << 28, "e2m1")])
+def test_more_tokens_than_the_products_take_are_refused_before_weights_are_let_go_of(layer, T, fmt):
+    """Codes of the gathered rows past 2^32 - 2^20 bytes, rows past 2^29 or 2^31."""
+    layer.T = T
+    with pytest.raises(ValueError):
+        layer.pack_experts(fmt, keep=False)
+    assert layer.ex_w is not None and layer.packed is None and not layer._packed_room
