@@ -4,7 +4,7 @@
 // (sqrt(c2) sqrt(v) + eps), c1 and c2 the bias corrections; all in fp32.  Bound by HBM:
 // each element's weight and states are read and written once, its gradient read once.
 // The tensors' addresses travel in the launch's arguments, as many as 4 KB hold, so that
-// there is no table to copy to the device and a captured step holds them; a workgroup
+// there is no table to keep on the device and a captured step holds them; a workgroup
 // takes 4096 consecutive elements of one tensor, a lane four neighbouring ones at a time
 // (whole lines of fp32 per instruction; eight with 8-bit states, a tile of which is then
 // one row of 16 lanes), all of them in flight together.  A workgroup whose elements all
@@ -14,14 +14,16 @@
 // its root, whose range is the root of v's: a tile's roots reach from its largest down to
 // 2^-18 of it, v's values to 2^-36.  Codes are rounded stochastically: a step moves v by
 // about 1 - b2 of itself, far below half a step of the codes, and rounding to nearest
-// would leave it where it is for good.  The random numbers, the codes and the update are
+// would leave it where it is for good.  (The roundings spread the roots: a step's adds (1 - b2) / 32
+// to / 16 of a root's square to its variance, codes being 1/16 to 1/8 apart, and of the sum about
+// 1 / 2 (1 - b2) steps' last: a deviation of 11 to 18 %.)  The random numbers, the codes and the update are
 // arithmetic enough to bound this form (12 bytes and 56 vector instructions an element):
 // hence one root for the update and the code, square root and reciprocal from the
 // hardware's instructions (1 ulp each, against 20 instructions of the exact division),
 // and the conversion that rounds by given random bits.  Measured, of 1.46 x 10^9 bf16
 // weights without a master, fp32 gradients: 3.2 ms, 5.4 TB/s (4.9 ms with two exact roots,
-// an exact division and rounding in integers); 0.81 x 10^9 with masters and fp32 states:
-// 4.3 to 4.5 ms, 5.4 to 5.7 TB/s.
+// an exact division and rounding in integers); 0.81 x 10^9 with masters and fp32 states, 30
+// bytes each: 4.3 to 4.5 ms, 5.4 to 5.7 TB/s.
 #include "mx.h"
 
 #include <math.h>

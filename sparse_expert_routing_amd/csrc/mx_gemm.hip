@@ -27,11 +27,14 @@
 // BM by the average rows of a group; k_mx_few where the tiles are few.
 //
 // Measured.  512 rows on 256 experts, 2048 x 7168, e4m3 rows: 260 to 290 us, the 1.72 GB of
-// weights that have rows at 5.9 TB/s or more: bound by HBM.  131072 rows on 32 experts, 7168 x
-// 2048, e2m1 rows: 1.19 to 1.24 ms, 3.2 PFLOP/s; the gate and up of 131072 rows on 256 experts,
-// 2048 x 7168, e4m3 rows: 3.75 to 3.99 ms, 2.0 PFLOP/s: bound by the card's power (1.85 to
-// 1.97 GHz with data, 2.3 to 2.4 with zeros; without the loads of x in the same cycles), at
-// 2540 cycles a stage of which the matrix instructions take 2048.
+// weights that have rows at 5.9 TB/s or more (a sixth of them from the Infinity Cache, from
+// pass to pass): bound by HBM.  131072 rows on 32 experts, 7168 x 2048, e2m1 rows: 1.19 to
+// 1.25 ms, 3.1 to 3.2 PFLOP/s; the gate and up of 131072 rows on 256 experts, 2048 x 7168, e4m3
+// rows: 3.75 to 3.99 ms, 2.0 PFLOP/s.  These are bound by the cycles of a tile first: a stage
+// takes 2540 where its matrix instructions need 2048 (one wave to a SIMD, nothing beside it), and
+// a tile's begin and end some 13000 without any, of 34600 in all at K = 2048, 48800 at 7168.
+// Without the loads of x the cycles are the same.  The card's power is the smaller part: of
+// operands of zeros the same calls take 1.09 ms, and the whole FFN 4.75 where it takes 5.7 to 5.8.
 #include "mx.h"
 
 namespace moe {
@@ -929,7 +932,9 @@ int rows_of_group(int M, int G) { return (M + G - 1) / G; }
 // Tiles of 32 rows x 256 weight rows up to which k_mx_few takes a product.  Measured, few
 // against tiles in us, e4m3, K = 2048 unless given: 1 row x 7168 (28) 4.7 against 10.5; 1 x
 // 2048, K = 7168 (8) 7.9 against 26.4; 8 groups' row x 4096, K = 7168 (128) 25.7 against
-// 29.3; 128 x 7168 (140) 17.3 against 28.1; 8 groups' row x 7168 (224) 20.2 against 14.2.
+// 29.3; 128 x 7168 (140) 17.3 against 28.1; 8 groups' row x 7168 (224) 20.2 against 14.2.  That
+// border comes early where one group has many rows: of 4096 x 4096, 319 rows (160) take 32.8 us by
+// few, 320 rows 49.3 by tiles of 256 rows, of which there are 32 for 256 CUs.
 constexpr int kFewTiles = 160;
 int64_t row_tiles(int G, int M) { return M < M / 32 + G ? M : M / 32 + G; }  // of 32 rows, at most
 bool few(int G, int M, int N) { return row_tiles(G, M) * ((N + BN - 1) / BN) <= kFewTiles; }
