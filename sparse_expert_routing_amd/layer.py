@@ -229,7 +229,7 @@ class MoeLayer:
         if not keep:
             # the packing on its stream, and forwards on any other: freed before those have read them, the weights' memory
             # would be handed out anew on the stream that they were allocated on
-            torch.cuda.synchronize(self.device)
+            torch.cuda.synchronize(self.ex["gate"].device)
             self.ex.update(gate=None, up=None, down=None)
             self.ex_w = None
 

@@ -40,3 +40,13 @@ def test_more_tokens_than_the_products_take_are_refused_before_weights_are_let_g
     with pytest.raises(ValueError):
         layer.pack_experts(fmt, keep=False)
     assert layer.ex_w is not None and layer.packed is None and not layer._packed_room
+
+
+def test_the_device_that_is_waited_for_is_the_weights(layer, monkeypatch):
+    """A layer made on "cuda" lies on the device that was current then, not on the one that is."""
+    waited = []
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: waited.append(device))
+    where = layer.ex["gate"].device
+    layer.device = torch.device("meta")
+    layer.pack_experts(keep=False)
+    assert waited == [where]
