@@ -30,11 +30,13 @@
 // weights that have rows at 5.9 TB/s or more (a sixth of them from the Infinity Cache, from
 // pass to pass): bound by HBM.  131072 rows on 32 experts, 7168 x 2048, e2m1 rows: 1.19 to
 // 1.25 ms, 3.1 to 3.2 PFLOP/s; the gate and up of 131072 rows on 256 experts, 2048 x 7168, e4m3
-// rows: 3.75 to 3.99 ms, 2.0 PFLOP/s.  These are bound by the cycles of a tile first: a stage
-// takes 2540 where its matrix instructions need 2048 (one wave to a SIMD, nothing beside it), and
-// a tile's begin and end some 13000 without any, of 34600 in all at K = 2048, 48800 at 7168.
-// Without the loads of x the cycles are the same.  The card's power is the smaller part: of
-// operands of zeros the same calls take 1.09 ms, and the whole FFN 4.75 where it takes 5.7 to 5.8.
+// rows: 3.75 to 3.99 ms, 2.0 PFLOP/s.  These are bound by the cycles of a tile first, with one
+// wave to a SIMD and nothing beside it.  Counted in the kernel at K = 2048, a tile of e2m1 rows
+// takes 43500 (some 39600 without the counters): the epilogue 9000, the next tile's setup 4500,
+// eight stages 3690 each where the matrix instructions need 2048, waits and barriers 1500 of it
+// all; one of e4m3 rows 58500: 8800, 7900 and sixteen stages of 2620.  Without the loads of x the
+// cycles are the same.  The card's power is the smaller part: of operands of zeros the product
+// takes 1.09 ms, and the whole FFN 4.75 where it takes 5.7 to 5.8.
 #include "mx.h"
 
 namespace moe {
